@@ -6,10 +6,11 @@ CPU fallback: without the built library or a CUDA device every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
-from typing import Optional
+from typing import Optional, Union
 
 import torch
 
@@ -41,7 +42,9 @@ EXPORTS = ("aaac_workspace_size", "aaac_importance", "aaac_init_codebooks", "aaa
            "aaac_pack_sharded", "aaac_linear_workspace_size", "aaac_linear_ws",
            "aaac_fit_launch_plan", "aaac_linear_launch_plan", "aaac_inject_fault",
            "aaac_device_checks",
-           "aaac_checked_build")
+           "aaac_checked_build", "aaac_mx_scale_bytes", "aaac_mx_quantize", "aaac_mx_dequant",
+           "aaac_mx_linear", "aaac_mx_workspace_size", "aaac_mx_linear_ws",
+           "aaac_mx_launch_plan")
 
 
 # reduction callback of the row-sharded calls: (user, buf, count, op, stream) -> 0 | error
@@ -161,6 +164,21 @@ def load(path: str = LIB_PATH):
     L.aaac_fit_layer_sharded.argtypes = [P, i64, i64, i64, P, P, P, P, P, P, R, P, P, sz, P]
     L.aaac_pack_sharded.restype = ctypes.c_int
     L.aaac_pack_sharded.argtypes = [P, i64, i64, i64, P, P, P, P, P, P, P, P, P, R, P, P, sz, P]
+    i32 = ctypes.c_int32
+    L.aaac_mx_scale_bytes.restype = sz
+    L.aaac_mx_scale_bytes.argtypes = [i32, i64, i64, i32]
+    L.aaac_mx_quantize.restype = ctypes.c_int
+    L.aaac_mx_quantize.argtypes = [P, P, P]
+    L.aaac_mx_dequant.restype = ctypes.c_int
+    L.aaac_mx_dequant.argtypes = [P, P, i32, i64, P]
+    L.aaac_mx_linear.restype = ctypes.c_int
+    L.aaac_mx_linear.argtypes = [P, P, P, i32, i64, P]
+    L.aaac_mx_workspace_size.restype = sz
+    L.aaac_mx_workspace_size.argtypes = [i32, i64, i64, i32]
+    L.aaac_mx_linear_ws.restype = ctypes.c_int
+    L.aaac_mx_linear_ws.argtypes = [P, i64, P, P, P, i32, i64, P, sz, P]
+    L.aaac_mx_launch_plan.restype = ctypes.c_int
+    L.aaac_mx_launch_plan.argtypes = [i32, i64, i64, i64, ctypes.POINTER(i32)]
     _lib = L
     return L
 
@@ -482,6 +500,209 @@ def awq_fit(W: torch.Tensor, I: torch.Tensor, tokens: int, cfg: Config, alphas16
                                _ptr(out["choice_bits"]), _ptr(out["err_final"]),
                                _ptr(out["err_alpha"]), _ptr(out["best"]), _ptr(ws), ws.numel(),
                                _stream(stream)))
+    return out
+
+
+# --------------------------------------------------------------------------
+# microscaled 4-bit tensors: quantisation, the way back, and the product
+# --------------------------------------------------------------------------
+MX_E8M0 = 0  # blocks of 32, power-of-two scales
+MX_E4M3 = 1  # blocks of 16, E4M3 scales, a power of two per row
+MX_SWIGLU = 1
+_MX_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+class CMxTensor(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("groups", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("row_scale", ctypes.c_void_p), ("offsets", ctypes.c_void_p)]
+
+
+class CMxSource(ctypes.Structure):
+    _fields_ = [("X", ctypes.c_void_p), ("type", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("rows", ctypes.c_int64), ("ldx", ctypes.c_int64), ("index", ctypes.c_void_p)]
+
+
+def mx_scale_bytes(fmt: int, rows: int, K: int, groups: int = 1) -> int:
+    """Bytes of a microscaled tensor's scales (see aaac_mx_tensor)."""
+    return int(load().aaac_mx_scale_bytes(fmt, rows, K, groups))
+
+
+def mx_workspace_size(fmt: int, rows: int, K: int, groups: int = 1) -> int:
+    """Bytes of the workspace in which mx_linear quantises its activations."""
+    return int(load().aaac_mx_workspace_size(fmt, rows, K, groups))
+
+
+def mx_launch_plan(groups: int, rows: int, N: int, K: int) -> dict:
+    """Host-only: the product's plan for these sizes (see aaac_mx_launch_plan)."""
+    out = (ctypes.c_int32 * 5)()
+    _check(load().aaac_mx_launch_plan(groups, rows, N, K, out))
+    return dict(zip(("columns", "split", "ctas", "stages", "tiles"), list(out)))
+
+
+class MxTensor:
+    """A microscaled 4-bit tensor on the device (aaac_mx_tensor): codes uint8
+    [rows, K/2], scales uint8 (mx_scale_bytes of them), row_scale fp32 [rows]
+    (MX_E4M3).  Its rows come in `groups` groups: equal ones, or
+    offsets[e] : offsets[e + 1] (int32 [groups + 1])."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor,
+                 row_scale: Optional[torch.Tensor], fmt: int, groups: int = 1,
+                 offsets: Optional[torch.Tensor] = None):
+        self.codes, self.scales, self.row_scale = codes, scales, row_scale
+        self.fmt, self.groups, self.offsets = fmt, groups, offsets
+        self.rows, self.K = codes.shape[0], 2 * codes.shape[1]
+        if codes.dtype != torch.uint8 or not codes.is_contiguous():
+            raise ValueError("codes must be contiguous uint8 [rows, K/2]")
+        need = mx_scale_bytes(fmt, self.rows, self.K, groups)
+        if scales.dtype != torch.uint8 or not scales.is_contiguous() or scales.numel() < need:
+            raise ValueError(f"scales must be contiguous uint8, {need} bytes")
+        if fmt == MX_E4M3 and (row_scale is None or row_scale.dtype != torch.float32
+                               or not row_scale.is_contiguous()
+                               or row_scale.numel() < self.rows):
+            raise ValueError(f"row_scale must be contiguous float32 [{self.rows}]")
+        _mx_offsets(offsets, groups)
+        same = [t for t in (scales, row_scale if fmt == MX_E4M3 else None, offsets)
+                if t is not None]
+        if any(t.device != codes.device for t in same):
+            raise ValueError("the parts of a microscaled tensor lie on different devices")
+        self._c = CMxTensor(fmt, groups, self.rows, self.K, _ptr(codes), _ptr(scales),
+                            _ptr(row_scale) if fmt == MX_E4M3 else None, _ptr(offsets))
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @staticmethod
+    def empty(fmt: int, rows: int, K: int, groups: int = 1,
+              offsets: Optional[torch.Tensor] = None, device="cuda") -> "MxTensor":
+        need = mx_scale_bytes(fmt, rows, K, groups)
+        if need == 0:
+            raise AaacError(2, load().aaac_last_error().decode())
+        return MxTensor(torch.empty(rows, K // 2, dtype=torch.uint8, device=device),
+                        torch.empty(need, dtype=torch.uint8, device=device),
+                        (torch.empty(rows, dtype=torch.float32, device=device)
+                         if fmt == MX_E4M3 else None), fmt, groups, offsets)
+
+
+def _mx_offsets(offsets: Optional[torch.Tensor], groups: int) -> None:
+    if offsets is not None and (offsets.dtype != torch.int32 or not offsets.is_contiguous()
+                                or offsets.numel() != groups + 1):
+        raise ValueError(f"offsets must be contiguous int32 [{groups + 1}]")
+
+
+def _mx_on(device, *tensors) -> None:
+    """Every tensor on `device`, and that the current one: the library launches there."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {t.device} and {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _scope(stream):
+    """What a call allocates for itself belongs to the stream it runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _mx_source(X: torch.Tensor, rows: Optional[torch.Tensor], swiglu: bool):
+    """(aaac_mx_source, quantised rows, K, the tensor it points into)."""
+    if X.dtype not in _MX_TYPES or X.dim() != 2:
+        raise ValueError("X must be a bfloat16 or float32 matrix")
+    if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1
+                             or not rows.is_contiguous()):
+        raise ValueError("rows must be contiguous int32 [quantised rows]")
+    n, width = X.shape
+    if (X.stride(1) != 1 or X.stride(0) * X.element_size() % 16 or X.stride(0) < width
+            or X.data_ptr() % 16):
+        X = X.contiguous()
+    src = CMxSource(_ptr(X), _MX_TYPES[X.dtype], MX_SWIGLU if swiglu else 0, n, X.stride(0),
+                    _ptr(rows))
+    return src, n if rows is None else rows.numel(), width // 2 if swiglu else width, X
+
+
+def _mx_out(out: Optional[torch.Tensor], rows: int, cols: int, dtype, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(rows, cols, dtype=dtype, device=device)
+    if (out.shape != (rows, cols) or out.dtype not in _MX_TYPES
+            or (cols > 1 and out.stride(1) != 1)):
+        raise ValueError(f"out must be a bfloat16 or float32 [{rows}, {cols}] with "
+                         "consecutive columns")
+    return out
+
+
+def _ld(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def mx_quantize(X: torch.Tensor, fmt: int, rows: Optional[torch.Tensor] = None,
+                swiglu: bool = False, groups: int = 1,
+                offsets: Optional[torch.Tensor] = None, out: Optional[MxTensor] = None,
+                stream=None) -> MxTensor:
+    """Rows of X (bf16 or fp32 [n, K]) as a microscaled 4-bit tensor.  rows
+    (int32) picks the source row of each quantised row (-1: a row of zeros);
+    swiglu quantises silu(a) * b of X's two halves [n, 2K]; groups and offsets
+    are the rows' groups (see MxTensor)."""
+    _need_cuda()
+    with _scope(stream):
+        src, n, K, X = _mx_source(X, rows, swiglu)
+        if out is None:
+            _mx_offsets(offsets, groups)
+            out = MxTensor.empty(fmt, n, K, groups, offsets, X.device)
+        elif (out.fmt, out.rows, out.K) != (fmt, n, K):
+            raise ValueError(f"out is fmt {out.fmt} [{out.rows}, {out.K}], not {fmt} [{n}, {K}]")
+        _mx_on(X.device, rows, out.codes)
+        _check(load().aaac_mx_quantize(ctypes.byref(src), ctypes.byref(out._c),
+                                       _stream(stream)))
+    return out
+
+
+def mx_dequant(q: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """A microscaled tensor's values, bf16 or fp32 [rows, K]."""
+    _need_cuda()
+    with _scope(stream):
+        out = _mx_out(out, q.rows, q.K, dtype, q.device)
+        _mx_on(q.device, out)
+        _check(load().aaac_mx_dequant(ctypes.byref(q._c), _ptr(out), _MX_TYPES[out.dtype],
+                                      _ld(out), _stream(stream)))
+    return out
+
+
+def mx_linear(X: Union[torch.Tensor, MxTensor], W: MxTensor, out: Optional[torch.Tensor] = None,
+              out_dtype=torch.float32, rows: Optional[torch.Tensor] = None, swiglu: bool = False,
+              offsets: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """Y[rows, N] = X @ W^T on the 4-bit tensor cores; with W.groups > 1 each
+    group of X's rows (an expert's) meets its own N rows of W.  X is a
+    microscaled tensor, or bf16 / fp32 activations that are quantised here as
+    mx_quantize does (rows, swiglu and offsets as there; ws: a workspace of
+    mx_workspace_size bytes)."""
+    _need_cuda()
+    with _scope(stream):
+        N = W.rows // W.groups
+        if isinstance(X, MxTensor):
+            if rows is not None or swiglu or offsets is not None or ws is not None:
+                raise ValueError("rows, swiglu, offsets and ws go with activations that are "
+                                 "not quantised yet")
+            out = _mx_out(out, X.rows, N, out_dtype, X.device)
+            _mx_on(X.device, W.codes, out)
+            _check(load().aaac_mx_linear(ctypes.byref(X._c), ctypes.byref(W._c), _ptr(out),
+                                         _MX_TYPES[out.dtype], _ld(out), _stream(stream)))
+            return out
+        src, n, K, X = _mx_source(X, rows, swiglu)
+        if K != W.K:
+            raise ValueError(f"X has K={K}, W has K={W.K}")
+        _mx_offsets(offsets, W.groups)
+        out = _mx_out(out, n, N, out_dtype, X.device)
+        if ws is None:
+            ws = torch.empty(mx_workspace_size(W.fmt, n, K, W.groups), dtype=torch.uint8,
+                             device=X.device)
+        _mx_on(X.device, rows, offsets, W.codes, out, ws)
+        _check(load().aaac_mx_linear_ws(ctypes.byref(src), n, _ptr(offsets), ctypes.byref(W._c),
+                                        _ptr(out), _MX_TYPES[out.dtype], _ld(out), _ptr(ws),
+                                        ws.numel(), _stream(stream)))
     return out
 
 

@@ -15,6 +15,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "mx.cuh"
 
 namespace aaac {
 static std::atomic<unsigned long long> g_launches{0};
@@ -618,6 +619,206 @@ aaac_status aaac_linear_ws(const void* X, int64_t M, int64_t ldx, const uint8_t*
   return from_cuda(e, "aaac_linear_ws");
 }
 
+// ---- microscaled 4-bit tensors ----------------------------------------------
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static aaac_status check_mx_shape(int fmt, int64_t rows, int64_t K, int64_t groups) {
+  if (fmt != AAAC_MX_E8M0 && fmt != AAAC_MX_E4M3)
+    return fail(AAAC_ERR_UNSUPPORTED, "fmt %d is not AAAC_MX_E8M0 or AAAC_MX_E4M3", fmt);
+  if (rows < 0 || rows > INT32_MAX)
+    return fail(AAAC_ERR_SHAPE, "rows=%lld must be in [0, 2^31)", (long long)rows);
+  if (K <= 0 || K % 32 || K > ((int64_t)1 << 24))
+    return fail(AAAC_ERR_SHAPE, "K=%lld must be a multiple of 32 in [32, 2^24]", (long long)K);
+  if (groups < 1 || groups > aaac::kMxMaxGroups)
+    return fail(AAAC_ERR_SHAPE, "groups=%lld must be in [1, %d]", (long long)groups,
+                aaac::kMxMaxGroups);
+  return AAAC_OK;
+}
+
+static aaac_status check_mx(const aaac_mx_tensor* t, const char* name) {
+  if (!t) return fail(AAAC_ERR_INVALID_ARG, "%s is NULL", name);
+  CHECK(check_mx_shape(t->fmt, t->rows, t->K, t->groups));
+  if (!t->offsets && t->rows % t->groups)
+    return fail(AAAC_ERR_SHAPE, "%s: %lld rows do not split into %d equal groups", name,
+                (long long)t->rows, t->groups);
+  if (!aligned4(t->offsets)) return fail(AAAC_ERR_ALIGN, "%s: offsets is not 4-byte aligned", name);
+  if (t->rows == 0) return AAAC_OK;
+  CHECK(check_ptr(t->codes, "codes"));
+  CHECK(check_ptr(t->scales, "scales"));
+  if (t->fmt == AAAC_MX_E4M3) {
+    if (!t->row_scale) return fail(AAAC_ERR_INVALID_ARG, "%s: row_scale is NULL", name);
+    if (!aligned4(t->row_scale))
+      return fail(AAAC_ERR_ALIGN, "%s: row_scale is not 4-byte aligned", name);
+  }
+  return AAAC_OK;
+}
+
+static aaac_status check_mx_source(const aaac_mx_source* x, int64_t rows, int64_t K) {
+  if (!x) return fail(AAAC_ERR_INVALID_ARG, "source is NULL");
+  if (x->type != AAAC_BF16 && x->type != AAAC_F32)
+    return fail(AAAC_ERR_UNSUPPORTED, "type %d is not AAAC_BF16 or AAAC_F32", x->type);
+  if (x->flags & ~(uint32_t)AAAC_MX_SWIGLU)
+    return fail(AAAC_ERR_INVALID_ARG, "unknown flags 0x%x", x->flags);
+  const int64_t width = x->flags & AAAC_MX_SWIGLU ? 2 * K : K;
+  if (x->rows < 0 || x->rows > INT32_MAX)
+    return fail(AAAC_ERR_SHAPE, "source rows=%lld must be in [0, 2^31)", (long long)x->rows);
+  if (!x->index && x->rows != rows)
+    return fail(AAAC_ERR_SHAPE, "source has %lld rows, the tensor %lld, and there is no index",
+                (long long)x->rows, (long long)rows);
+  if (x->ldx < width)
+    return fail(AAAC_ERR_SHAPE, "ldx=%lld < %lld", (long long)x->ldx, (long long)width);
+  if (x->ldx > ((int64_t)1 << 31))
+    return fail(AAAC_ERR_SHAPE, "ldx=%lld is above 2^31", (long long)x->ldx);
+  if (x->ldx % (x->type == AAAC_F32 ? 4 : 8))
+    return fail(AAAC_ERR_ALIGN, "ldx=%lld: rows are not 16-byte aligned", (long long)x->ldx);
+  if (!aligned4(x->index)) return fail(AAAC_ERR_ALIGN, "index is not 4-byte aligned");
+  if (rows > 0 && x->rows > 0) CHECK(check_ptr(x->X, "X"));
+  return AAAC_OK;
+}
+
+static aaac_status check_mx_out(const void* Y, int type, int64_t ldy, int64_t width, int64_t rows,
+                                int align) {
+  if (type != AAAC_BF16 && type != AAAC_F32)
+    return fail(AAAC_ERR_UNSUPPORTED, "type %d is not AAAC_BF16 or AAAC_F32", type);
+  if (ldy < width)
+    return fail(AAAC_ERR_SHAPE, "leading dimension %lld < %lld", (long long)ldy, (long long)width);
+  if (ldy > ((int64_t)1 << 31))
+    return fail(AAAC_ERR_SHAPE, "leading dimension %lld is above 2^31", (long long)ldy);
+  if (rows == 0) return AAAC_OK;
+  if (!Y) return fail(AAAC_ERR_INVALID_ARG, "output is NULL");
+  const int size = type == AAAC_F32 ? 4 : 2;
+  const int unit = align > size ? align : size;
+  if (reinterpret_cast<uintptr_t>(Y) % unit || ldy * size % unit)
+    return fail(AAAC_ERR_ALIGN, "output rows are not %d-byte aligned", unit);
+  return AAAC_OK;
+}
+
+static aaac::MxTensor mx_of(const aaac_mx_tensor* t) {
+  return aaac::MxTensor{t->codes, t->scales, t->row_scale, t->offsets, t->fmt, t->groups,
+                        t->rows, t->K};
+}
+
+static aaac::MxSource mx_source_of(const aaac_mx_source* x) {
+  return aaac::MxSource{x->X, x->index, x->ldx, x->rows, x->type == AAAC_F32,
+                        (x->flags & AAAC_MX_SWIGLU) != 0};
+}
+
+// The product's own checks: X's rows against W's groups of N rows each.
+static aaac_status check_mx_product(int fmt, int64_t rows, int64_t K, int64_t groups,
+                                    const aaac_mx_tensor* w) {
+  CHECK(check_mx(w, "w"));
+  if (w->offsets) return fail(AAAC_ERR_INVALID_ARG, "w: weights have groups of equal size");
+  if (w->rows == 0) return fail(AAAC_ERR_SHAPE, "w has no rows");
+  if (fmt != w->fmt) return fail(AAAC_ERR_INVALID_ARG, "x has fmt %d, w %d", fmt, w->fmt);
+  if (K != w->K)
+    return fail(AAAC_ERR_SHAPE, "x has K=%lld, w %lld", (long long)K, (long long)w->K);
+  if (groups != w->groups)
+    return fail(AAAC_ERR_SHAPE, "x has %lld groups, w %d", (long long)groups, w->groups);
+  const int64_t n_tiles = (w->rows / w->groups + 127) / 128;
+  if ((rows / 32 + groups) * n_tiles > INT32_MAX)
+    return fail(AAAC_ERR_SHAPE, "too many output tiles (rows=%lld, w rows=%lld)", (long long)rows,
+                (long long)w->rows);
+  return AAAC_OK;
+}
+
+size_t aaac_mx_scale_bytes(int32_t fmt, int64_t rows, int64_t K, int32_t groups) {
+  if (check_mx_shape(fmt, rows, K, groups) != AAAC_OK) return 0;
+  return aaac::mx_scale_bytes(fmt, rows, K, groups);
+}
+
+aaac_status aaac_mx_quantize(const aaac_mx_source* src, const aaac_mx_tensor* q, void* stream) {
+  CallScope cs_("aaac_mx_quantize");
+  CHECK(check_mx(q, "q"));
+  CHECK(check_mx_source(src, q->rows, q->K));
+  CHECK(take_fault());
+  if (q->rows == 0) return ok();
+  aaac::count_launches(1);
+  return from_cuda(aaac::launch_mx_quantize(mx_source_of(src), mx_of(q), (cudaStream_t)stream),
+                   "aaac_mx_quantize");
+}
+
+aaac_status aaac_mx_dequant(const aaac_mx_tensor* q, void* out, int32_t type, int64_t ldo,
+                            void* stream) {
+  CallScope cs_("aaac_mx_dequant");
+  CHECK(check_mx(q, "q"));
+  CHECK(check_mx_out(out, type, ldo, q->K, q->rows, 16));
+  CHECK(take_fault());
+  if (q->rows == 0) return ok();
+  aaac::count_launches(1);
+  return from_cuda(
+      aaac::launch_mx_dequant(mx_of(q), out, type == AAAC_F32, ldo, (cudaStream_t)stream),
+      "aaac_mx_dequant");
+}
+
+aaac_status aaac_mx_linear(const aaac_mx_tensor* x, const aaac_mx_tensor* w, void* Y,
+                           int32_t type, int64_t ldy, void* stream) {
+  CallScope cs_("aaac_mx_linear");
+  CHECK(check_mx(x, "x"));
+  CHECK(check_mx_product(x->fmt, x->rows, x->K, x->groups, w));
+  CHECK(check_mx_out(Y, type, ldy, w->rows / w->groups, x->rows, 1));
+  CHECK(take_fault());
+  if (x->rows == 0) return ok();
+  aaac::count_launches(1);
+  return from_cuda(aaac::launch_mx_gemm(mx_of(x), mx_of(w), Y, type == AAAC_F32, ldy, false,
+                                        (cudaStream_t)stream),
+                   "aaac_mx_linear");
+}
+
+size_t aaac_mx_workspace_size(int32_t fmt, int64_t rows, int64_t K, int32_t groups) {
+  if (check_mx_shape(fmt, rows, K, groups) != AAAC_OK) return 0;
+  return aaac::align256((size_t)rows * (size_t)(K / 2)) +
+         aaac::align256(aaac::mx_scale_bytes(fmt, rows, K, groups)) +
+         aaac::align256((size_t)rows * sizeof(float));
+}
+
+aaac_status aaac_mx_linear_ws(const aaac_mx_source* src, int64_t rows, const int32_t* offsets,
+                              const aaac_mx_tensor* w, void* Y, int32_t type, int64_t ldy,
+                              void* ws, size_t ws_bytes, void* stream) {
+  CallScope cs_("aaac_mx_linear_ws");
+  CHECK(check_mx(w, "w"));
+  CHECK(check_mx_shape(w->fmt, rows, w->K, w->groups));
+  CHECK(check_mx_product(w->fmt, rows, w->K, w->groups, w));
+  if (!offsets && rows % w->groups)
+    return fail(AAAC_ERR_SHAPE, "%lld rows do not split into %d equal groups", (long long)rows,
+                w->groups);
+  if (!aligned4(offsets)) return fail(AAAC_ERR_ALIGN, "offsets is not 4-byte aligned");
+  CHECK(check_mx_source(src, rows, w->K));
+  CHECK(check_mx_out(Y, type, ldy, w->rows / w->groups, rows, 1));
+  if (rows > 0) CHECK(check_ws(ws, ws_bytes, aaac_mx_workspace_size(w->fmt, rows, w->K, w->groups)));
+  CHECK(take_fault());
+  if (rows == 0) return ok();
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  aaac::MxTensor x;
+  x.fmt = w->fmt;
+  x.groups = w->groups;
+  x.rows = rows;
+  x.K = w->K;
+  x.offsets = offsets;
+  x.codes = base;
+  x.scales = base + aaac::align256((size_t)rows * (size_t)(w->K / 2));
+  x.row_scale = reinterpret_cast<float*>(
+      x.scales + aaac::align256(aaac::mx_scale_bytes(w->fmt, rows, w->K, w->groups)));
+  cudaError_t e = aaac::launch_mx_quantize(mx_source_of(src), x, (cudaStream_t)stream);
+  if (e == cudaSuccess)
+    e = aaac::launch_mx_gemm(x, mx_of(w), Y, type == AAAC_F32, ldy, true, (cudaStream_t)stream);
+  if (e == cudaSuccess) aaac::count_launches(2);
+  return from_cuda(e, "aaac_mx_linear_ws");
+}
+
+aaac_status aaac_mx_launch_plan(int32_t groups, int64_t rows, int64_t N, int64_t K, int32_t* out) {
+  if (!out) return fail(AAAC_ERR_INVALID_ARG, "out is NULL");
+  CHECK(check_mx_shape(AAAC_MX_E4M3, rows, K, groups));
+  if (rows < 1 || N < 1 || N > INT32_MAX || (rows / 32 + groups) * ((N + 127) / 128) > INT32_MAX)
+    return fail(AAAC_ERR_SHAPE, "rows=%lld or N=%lld out of range", (long long)rows, (long long)N);
+  const aaac::MxPlan p = aaac::mx_plan(groups, rows, N, K);
+  out[0] = p.nt;
+  out[1] = p.split;
+  out[2] = p.ctas;
+  out[3] = p.stages;
+  out[4] = (int32_t)p.tiles;
+  return ok();
+}
+
 aaac_status aaac_device_checks(uint32_t* flag) {
   if (!flag) return fail(AAAC_ERR_INVALID_ARG, "flag is NULL");
   unsigned int vf = 0, vi = 0;
@@ -647,10 +848,11 @@ aaac_status aaac_inject_fault(const char* kind) {
 
 aaac_status aaac_device_timeouts(uint32_t* flag) {
   if (!flag) return fail(AAAC_ERR_INVALID_ARG, "flag is NULL");
-  unsigned int v = 0;
-  const cudaError_t e = aaac::gemm_timeout_flag(&v);
+  unsigned int v = 0, vm = 0;
+  cudaError_t e = aaac::gemm_timeout_flag(&v);
+  if (e == cudaSuccess) e = aaac::mx_timeout_flag(&vm);
   if (e != cudaSuccess) return from_cuda(e, "aaac_device_timeouts");
-  *flag = v ? 1u : 0u;
+  *flag = v || vm ? 1u : 0u;
   return AAAC_OK;
 }
 

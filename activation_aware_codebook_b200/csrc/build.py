@@ -21,7 +21,8 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libaaac.so")
 LIB_CHECKED = os.path.join(PKG, "libaaac_checked.so")
-SOURCES = ["api.cu", "importance.cu", "init.cu", "fit.cu", "linear.cu", "gemm.cu", "awq.cu"]
+SOURCES = ["api.cu", "importance.cu", "init.cu", "fit.cu", "linear.cu", "gemm.cu", "awq.cu",
+           "mx_quant.cu", "mx_gemm.cu"]
 BUILD_DIR = os.path.join(ROOT, "_build")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -139,4 +139,37 @@ cudaError_t launch_awq_keep(int j, const double* err_alpha, const void* const* s
                             void* const* dst, const size_t* bytes, int segs, double* err_final,
                             int32_t* best, cudaStream_t st);
 
+// ---- microscaled 4-bit tensors (mx_quant.cu, mx_gemm.cu) --------------------
+struct MxSource {
+  const void* X;
+  const int32_t* index;  // source row of each quantised row (NULL: the same row)
+  int64_t ldx, rows;     // of the source
+  bool f32, swiglu;
+};
+struct MxTensor {
+  uint8_t* codes;
+  uint8_t* scales;
+  float* row_scale;
+  const int32_t* offsets;
+  int fmt, groups;
+  int64_t rows, K;
+};
+struct MxPlan {
+  int nt;         // token columns of a tile
+  int split;      // CTAs that share a tile's K (1: persistent CTAs over the tiles)
+  int ctas;
+  int stages;     // 256-column stages of K
+  int64_t tiles;  // an upper bound for ragged groups
+};
+MxPlan mx_plan(int groups, int64_t rows, int64_t N, int64_t K);
+size_t mx_scale_bytes(int fmt, int64_t rows, int64_t K, int groups);
+cudaError_t launch_mx_quantize(const MxSource& x, const MxTensor& q, cudaStream_t st);
+cudaError_t launch_mx_dequant(const MxTensor& q, void* out, bool f32, int64_t ldo,
+                              cudaStream_t st);
+// overlap: the kernel before it on the stream is launch_mx_quantize's, and
+// everything but its outputs was ready before that one started
+cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f32, int64_t ldy,
+                           bool overlap, cudaStream_t st);
+cudaError_t mx_timeout_flag(unsigned int* out);
+
 }  // namespace aaac

@@ -1,0 +1,62 @@
+// mx.cuh -- the microscaled 4-bit layout that mx_quant.cu writes and
+// mx_gemm.cu reads.
+//
+// Values are E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two per
+// byte along K, the low nibble the even column: the order in which tcgen05
+// reads packed 4-bit operands.  The block scales lie as the tensor core wants
+// them in tensor memory: tiles of 128 rows x 4 blocks, 512 bytes each, row
+// i's four bytes at (i % 32) * 16 + (i / 32) * 4, so that one 32x128b copy
+// brings a tile in without any thread touching it.  Tiles of a row band are
+// consecutive along K.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace aaac {
+
+constexpr int kMxE8m0 = 0;  // blocks of 32, power-of-two scales
+constexpr int kMxE4m3 = 1;  // blocks of 16, E4M3 scales, a power of two per row
+constexpr int kMxTileRows = 128;
+constexpr int kMxTileBytes = 512;
+constexpr int kMxMaxGroups = 1024;
+
+__host__ __device__ constexpr int mx_block(int fmt) { return fmt == kMxE8m0 ? 32 : 16; }
+
+// Scale tiles along K (four blocks each; the last one is padded with zeros).
+__host__ __device__ inline int64_t mx_tiles_k(int fmt, int64_t K) {
+  const int64_t span = 4 * mx_block(fmt);
+  return (K + span - 1) / span;
+}
+
+// Rows of a tensor in groups (an expert's rows each): either `offsets`
+// (device, groups + 1 values) or groups of equal size.
+struct MxRows {
+  const int32_t* offsets;
+  int groups;
+  int rows;  // of all groups
+};
+
+// Group e's rows [first, last), held inside the tensor whatever the offsets say.
+__device__ __forceinline__ void mx_group(const MxRows& g, int e, int* first, int* last) {
+  if (g.offsets) {
+    const int a = min(max(__ldg(g.offsets + e), 0), g.rows);
+    *first = a;
+    *last = min(max(__ldg(g.offsets + e + 1), a), g.rows);
+  } else {
+    const int per = g.rows / g.groups;
+    *first = e * per;
+    *last = e * per + per;
+  }
+}
+
+// Each group's scales start a tile of their own: group e, whose first row is
+// `first`, starts at band first / 128 + e.  floor(a / 128) + floor(b / 128) <=
+// floor((a + b) / 128) keeps the bands of one group clear of the next one's,
+// and rows / 128 + groups bands hold them all, so a band follows from the
+// group's own offset with no sum over the others.
+__host__ __device__ inline int64_t mx_bands(int64_t rows, int groups) {
+  return rows / kMxTileRows + groups;
+}
+
+}  // namespace aaac

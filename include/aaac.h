@@ -25,7 +25,8 @@
  *  - Calls on one stream may share a workspace; concurrent calls on different
  *    streams need different workspaces.
  *  - NaN or infinite weights / activations are outside the contract: results
- *    are then unspecified, but every memory access stays in bounds.
+ *    are then unspecified, but every memory access stays in bounds (the
+ *    microscaled calls say what they do with them).
  */
 #ifndef AAAC_H
 #define AAAC_H
@@ -338,11 +339,113 @@ aaac_status aaac_linear_ws(const void* X, int64_t M, int64_t ldx, const uint8_t*
                            const uint16_t* T_bf16, int64_t N, int64_t K, const aaac_config* cfg,
                            float* Y, void* ws, size_t ws_bytes, void* stream);
 
+/* Microscaled 4-bit tensors: the tensor cores' own 4-bit format, for weights
+ * and activations (the summary's section 4 evaluates on NVFP4 layouts; this is
+ * that hardware format with its fixed E2M1 values in place of fitted
+ * codebooks, and with the activations in 4 bits too).
+ * A tensor of `rows` x K values holds E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and their negatives) under a scale for each block along K:
+ *   AAAC_MX_E8M0 : blocks of 32, scale 2^(byte - 127),
+ *                  byte = max(biased exponent of the block's amax - 2, 0);
+ *   AAAC_MX_E4M3 : blocks of 16, an E4M3 scale, and a power of two per row:
+ *                  g = 2^p, the smallest with row amax <= 2688 g (p >= -126;
+ *                  1 for a row of zeros), s = e4m3_RN(fp32_RN(amax / g / 6)).
+ *   code = E2M1_RN_sat(x / scale), ties to the even code; x / scale is the
+ *   fp32_RN quotient; codes of a zero scale are 0.
+ * NaN and infinity are inside this contract: an E8M0 block that holds one gets
+ * byte 255 (NaN), an E4M3 row that holds one gets row_scale NaN; what is
+ * computed from them is NaN.
+ * Rows come in `groups` groups (an expert's rows each): of equal size when
+ * offsets is NULL, else rows offsets[e] .. offsets[e + 1] - 1 are group e's
+ * (device int32 [groups + 1], ascending; groups may be empty; rows before
+ * offsets[0] or from offsets[groups] on belong to none, and no call reads or
+ * writes them).  Values of offsets outside [0, rows] are taken as the nearest
+ * bound; descending ones give unspecified values, and every access stays in
+ * bounds.
+ *   codes      [rows][K/2]: two per byte, low nibble = even k
+ *   scales     aaac_mx_scale_bytes() bytes: tiles of 128 rows x 4 blocks, 512
+ *              bytes each, row i's four bytes at (i % 32) * 16 + (i / 32) * 4;
+ *              the ceil(K / (4 * block)) tiles of a 128-row band follow one
+ *              another (blocks past K are 0), and group e, whose first row is
+ *              o, starts at band o / 128 + e
+ *   row_scale  fp32 [rows] (AAAC_MX_E4M3; ignored, may be NULL, for E8M0)
+ * K is a multiple of 32 up to 2^24, rows < 2^31, groups <= 1024.  codes and
+ * scales are 16-byte aligned, row_scale and offsets 4-byte. */
+typedef enum { AAAC_MX_E8M0 = 0, AAAC_MX_E4M3 = 1 } aaac_mx_format;
+typedef enum { AAAC_BF16 = 0, AAAC_F32 = 1 } aaac_type;
+
+typedef struct {
+    int32_t fmt;            /* aaac_mx_format                                  */
+    int32_t groups;         /* >= 1                                            */
+    int64_t rows, K;
+    uint8_t* codes;
+    uint8_t* scales;
+    float* row_scale;
+    const int32_t* offsets; /* or NULL                                         */
+} aaac_mx_tensor;
+
+/* Bytes of a tensor's scales (0 for invalid sizes). */
+size_t aaac_mx_scale_bytes(int32_t fmt, int64_t rows, int64_t K, int32_t groups);
+
+/* Rows to quantise: row r of the tensor comes from row index[r] of X (row r
+ * when index is NULL).  An index outside [0, rows) gives a row of zeros, so
+ * that -1 pads a batch.
+ *   AAAC_MX_SWIGLU: X's rows hold two halves of K columns, a and b, and
+ *     (a / (1 + exp(-a))) * b is quantised, computed in fp32. */
+#define AAAC_MX_SWIGLU 1u
+typedef struct {
+    const void* X;          /* device [rows][ldx], bf16 or fp32, 16-byte aligned rows */
+    int32_t type;           /* aaac_type                                       */
+    uint32_t flags;         /* AAAC_MX_SWIGLU                                  */
+    int64_t rows, ldx;      /* of X; ldx >= K (2K with AAAC_MX_SWIGLU)         */
+    const int32_t* index;   /* device int32 [tensor rows], 4-byte aligned, or NULL */
+} aaac_mx_source;
+
+/* Quantises src into q (q->codes, q->scales, q->row_scale are written).  The
+ * result of a row depends on that row alone.  q->rows == 0 does nothing. */
+aaac_status aaac_mx_quantize(const aaac_mx_source* src, const aaac_mx_tensor* q, void* stream);
+
+/* A tensor's values, E2M1 * scale * row_scale: exact in fp32 (6 significant
+ * bits), and in bf16 inside its range.
+ *   out   device bf16 or fp32 [rows][ldo], rows 16-byte aligned */
+aaac_status aaac_mx_dequant(const aaac_mx_tensor* q, void* out, int32_t type, int64_t ldo,
+                            void* stream);
+
+/* The product on the 4-bit tensor cores:
+ *   Y[m][n] = row_scale_x[m] * row_scale_w[n] * sum_k x[m][k] * w[e][n][k]
+ * where e is row m's group.  w's rows are `groups` groups (experts) of
+ * N = w->rows / groups rows each (w->offsets is NULL); x has as many groups,
+ * equal or ragged; groups = 1 is the plain linear layer.  Both have the same
+ * fmt and K.  The block scales are applied inside the tensor core and the sum
+ * is held in fp32, in a fixed order: two runs give the same bits.
+ *   Y    device fp32 or bf16 [rows][ldy], ldy >= N, element-aligned; rows of
+ *        no group are left as they were
+ * No workspace. */
+aaac_status aaac_mx_linear(const aaac_mx_tensor* x, const aaac_mx_tensor* w, void* Y,
+                           int32_t type, int64_t ldy, void* stream);
+
+/* aaac_mx_quantize and aaac_mx_linear in one call: Y from bf16 or fp32
+ * activations, quantised into the workspace; the product's kernel sets itself
+ * up and fetches its first weights while the quantisation runs.  rows and
+ * offsets are those of the quantised tensor (offsets NULL: equal groups).
+ *   ws   device, aaac_mx_workspace_size(w->fmt, rows, w->K, w->groups) bytes */
+size_t aaac_mx_workspace_size(int32_t fmt, int64_t rows, int64_t K, int32_t groups);
+aaac_status aaac_mx_linear_ws(const aaac_mx_source* src, int64_t rows, const int32_t* offsets,
+                              const aaac_mx_tensor* w, void* Y, int32_t type, int64_t ldy,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/* The product's plan for `rows` rows in `groups` groups, N weight rows per
+ * group and K columns.  A host-only query.  out (host int32[5]):
+ *   out[0]  token columns of a tile      out[1]  CTAs that share a tile's K
+ *   out[2]  CTAs                         out[3]  256-column stages of K
+ *   out[4]  output tiles (an upper bound when there is more than one group) */
+aaac_status aaac_mx_launch_plan(int32_t groups, int64_t rows, int64_t N, int64_t K, int32_t* out);
+
 /* Device-side wait status of the current device: *flag = 1 when a bounded
- * wait inside one of the library's kernels (the tensor-core aaac_linear path)
- * has run out since the library was loaded, else 0.  A kernel whose wait ran
- * out writes NaN to its output tile and still releases its tensor memory.
- * Synchronises with the device (reads a device variable). */
+ * wait inside one of the library's kernels (the tensor-core paths of aaac_linear
+ * and aaac_mx_linear) has run out since the library was loaded, else 0.  A
+ * kernel whose wait ran out writes NaN to its output tile and still releases
+ * its tensor memory.  Synchronises with the device (reads a device variable). */
 aaac_status aaac_device_timeouts(uint32_t* flag);
 
 /* Debug builds: 1 when the library was compiled with AAAC_CHECKS

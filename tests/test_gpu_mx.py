@@ -1,0 +1,436 @@
+"""Microscaled 4-bit tensors on the GPU: quantisation and dequantisation bit
+for bit against the format in 64-bit NumPy (tests/_mx.py), the product within
+the bound of its fp32 sums.
+
+Product's bound.  Every product of two E2M1 values under their block scales is
+exact, so the error is that of adding K terms in fp32 in some order: at most K
+additions, each off by less than one step (2^-23 relative to the partial sum's
+magnitude, whether the adder rounds or cuts), so |Y - exact| <= K 2^-23 S with
+S = sum |x w|.  The terms of one K = 64 step are added inside the tensor core,
+which leaves K / 64 additions of partial sums and 6 levels inside a step; the
+bound used is (K / 64 + 8) 2^-23 S, and half a step of bf16 (2^-8 relative)
+where the output is bf16.
+"""
+import numpy as np
+import pytest
+import torch
+
+import _mx
+from activation_aware_codebook_b200 import binding as bb
+from activation_aware_codebook_b200 import synth
+
+pytestmark = pytest.mark.gpu
+
+FMTS = [bb.MX_E8M0, bb.MX_E4M3]
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def activations(rows, K, seed, dtype=torch.bfloat16):
+    x = synth.make_activations(max(rows, 1), K, seed, True)[:rows]
+    if dtype == torch.float32:  # bits below bf16's
+        x = x.float() * (1.0 + 0.003 * torch.sin(torch.arange(K)))
+    return x
+
+
+def starts_of(rows, groups, offsets):
+    return list(range(0, rows + 1, rows // groups)) if offsets is None else list(offsets)
+
+
+def check_packed(q, x, starts):
+    """q's codes, scales and row scales against the reference for the rows of its groups."""
+    code, byte, g = _mx.quantize(x, q.fmt)
+    at = _mx.scale_index(q.rows, byte.shape[1], starts)
+    rows = np.arange(starts[0], starts[-1])
+    assert np.array_equal(q.codes.cpu().numpy()[rows], _mx.pack(code)[rows])
+    assert np.array_equal(q.scales.cpu().numpy()[at[rows]], byte[rows])
+    if q.fmt == bb.MX_E4M3:
+        assert np.array_equal(q.row_scale.cpu().numpy()[rows].astype(np.float64), g[rows],
+                              equal_nan=True)
+
+
+def values_of(q, starts):
+    code = _mx.unpack(q.codes.cpu().numpy())
+    at = _mx.scale_index(q.rows, q.K // _mx.BLOCK[q.fmt], starts)
+    g = q.row_scale.cpu().double().numpy() if q.fmt == bb.MX_E4M3 else None
+    return _mx.values(code, q.scales.cpu().numpy()[at], g, q.fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,K", [(1, 32), (3, 64), (130, 96), (257, 544), (5, 4096),
+                                    (2, 16448), (2, 32768), (1, 33024), (2, 65568)])
+def test_quantize_bit_exact(fmt, dtype, rows, K):
+    """Rows that fit one, two and more runs a thread, K of half a scale tile."""
+    x = activations(rows, K, rows + K, dtype)
+    q = bb.mx_quantize(x.cuda(), fmt)
+    check_packed(q, f64(x), [0, rows])
+    # the padding of the last tile along K is zero
+    words = -(-K // (4 * _mx.BLOCK[fmt]))
+    blocks = K // _mx.BLOCK[fmt]
+    last = q.scales.view(-1, words, 32, 4, 4)[:, -1, 0, 0].cpu().numpy()
+    if blocks % 4:
+        assert not last[0, blocks % 4:].any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_borders_and_extremes(fmt):
+    """Every border between codes and its neighbours under every scale, zeros,
+    subnormals, the largest numbers, and rows of one value."""
+    rows = []
+    s = 2.0 ** np.arange(-3, 5) if fmt == bb.MX_E8M0 else _mx.E4M3_VALUES[1:]
+    borders = np.concatenate([_mx.BORDERS, _mx.LEVELS[1:]])
+    for v in s:
+        cand = torch.tensor(borders * v, dtype=torch.float64).to(torch.bfloat16)
+        near = cand.view(torch.int16)
+        row = torch.zeros(64, dtype=torch.bfloat16)
+        row[:14] = cand
+        row[14:28] = (near + 1).view(torch.bfloat16)
+        row[28:42] = -(near - 1).view(torch.bfloat16)
+        rows.append(row)
+        row = row.clone()
+        row[32] = 2688.0  # the row's largest, in another block
+        rows.append(row)
+    tiny = torch.finfo(torch.bfloat16).tiny
+    for v in (0.0, -0.0, tiny, tiny / 64, 3e38, -3.3e38, 1e-30, 6.0, 7.5, 2688.0, 2720.0):
+        row = torch.zeros(64)
+        row[5] = v
+        row[40] = -v / 3
+        rows.append(row.to(torch.bfloat16))
+        rows.append(torch.full((64,), v).to(torch.bfloat16))
+    x = torch.stack(rows)
+    q = bb.mx_quantize(x.cuda(), fmt)
+    check_packed(q, f64(x), [0, x.shape[0]])
+    q = bb.mx_quantize(x.float().cuda(), fmt)
+    check_packed(q, f64(x), [0, x.shape[0]])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_nan_and_infinity_reach_the_output(fmt):
+    x = activations(6, 128, 3)
+    x[1, 40] = float("nan")
+    x[3, 7] = float("inf")
+    x[4, 127] = -float("inf")
+    q = bb.mx_quantize(x.cuda(), fmt)
+    check_packed(q, f64(x), [0, 6])
+    v = bb.mx_dequant(q, torch.float32)
+    ref = values_of(q, [0, 6])
+    assert np.array_equal(f64(v), ref, equal_nan=True)
+    W = bb.mx_quantize(activations(130, 128, 4).cuda(), fmt)
+    Y = bb.mx_linear(q, W).cpu()
+    assert torch.isnan(Y[[1, 3, 4]]).all() and torch.isfinite(Y[[0, 2, 5]]).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_swiglu(fmt, dtype):
+    """The same bits as quantising silu(a) * b computed in fp32 by torch, and
+    within one rounding of its 64-bit value (codes near a border may differ)."""
+    x = torch.cat([activations(67, 4640, 1, dtype), activations(67, 4640, 2, dtype)], 1)
+    x[3, :40] = torch.linspace(-120, 120, 40).to(dtype)
+    xg = x.cuda()
+    a, b = xg.float().chunk(2, 1)
+    h = a / (1.0 + torch.exp(-a)) * b
+    q, r = bb.mx_quantize(xg, fmt, swiglu=True), bb.mx_quantize(h, fmt)
+    assert torch.equal(q.codes, r.codes)
+    assert torch.equal(bb.mx_dequant(q), bb.mx_dequant(r))
+    a, b = f64(x)[:, :4640], f64(x)[:, 4640:]
+    with np.errstate(over="ignore"):
+        h64 = a / (1.0 + np.exp(-a)) * b
+    # exp, +, / and * in fp32: exp is within 2 steps, each other step half of
+    # one; above 88.73 fp32's exp(-a) is infinite, where the value is below
+    # 88.73 exp(-88.72) |b| < 3e-37 |b|
+    ok = np.abs(f64(h) - h64) <= 4 * 2.0 ** -23 * np.abs(h64) + 3e-37 * (1 + np.abs(b))
+    assert ok.all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_gather_groups_and_strides(fmt):
+    """Ragged groups (empty, one row, across tile bands), gathered rows with
+    padding and out-of-range indices, a strided source, and rows of no group
+    left as they were."""
+    K, n = 160, 90
+    offsets = [3, 3, 4, 140, 140, 270, 399, 400]
+    R = 404
+    src = activations(n, K + 24, 9)
+    x = src.cuda()[:, 8:8 + K]  # ldx = K + 24, rows 16-byte aligned
+    index = (torch.arange(R) * 7 % n).to(torch.int32)
+    index[10], index[200], index[300] = -1, n, 2 ** 31 - 1
+    ref = f64(src)[:, 8:8 + K][np.clip(index.numpy(), 0, n - 1)]
+    ref[[10, 200, 300]] = 0.0
+    out = bb.MxTensor.empty(fmt, R, K, len(offsets) - 1,
+                            torch.tensor(offsets, dtype=torch.int32).cuda())
+    out.codes.fill_(0x5A)
+    out.scales.fill_(0x5A)
+    if fmt == bb.MX_E4M3:
+        out.row_scale.fill_(-7.0)
+    bb.mx_quantize(x, fmt, rows=index.cuda(), out=out)
+    check_packed(out, ref, offsets)
+    outside = [0, 1, 2, 400, 401, 402, 403]
+    assert (out.codes[outside] == 0x5A).all()
+    if fmt == bb.MX_E4M3:
+        assert (out.row_scale[outside] == -7.0).all()
+    words = -(-K // (4 * _mx.BLOCK[fmt]))
+    at = _mx.scale_index(R, words * 4, offsets)
+    free = np.ones(out.scales.numel(), dtype=bool)
+    free[at[at >= 0]] = False
+    assert (out.scales.cpu().numpy()[free] == 0x5A).all()
+    # and back: rows of no group are not written either
+    back = torch.full((R, K), 11.0, dtype=torch.float32, device="cuda")
+    bb.mx_dequant(out, out=back)
+    code = _mx.unpack(out.codes.cpu().numpy())
+    g = out.row_scale.cpu().double().numpy() if fmt == bb.MX_E4M3 else None
+    at = _mx.scale_index(R, K // _mx.BLOCK[fmt], offsets)
+    v = _mx.values(code, out.scales.cpu().numpy()[np.maximum(at, 0)], g, fmt)
+    inside = np.arange(offsets[0], offsets[-1])
+    assert np.array_equal(f64(back)[inside], v[inside])
+    assert (back[outside] == 11.0).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows,K", [(1, 32), (129, 416), (300, 2080)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_dequant_exact(fmt, rows, K, dtype):
+    """Any codes and scales, not only those that quantisation makes; a strided output."""
+    r = np.random.RandomState(rows + K)
+    q = bb.MxTensor.empty(fmt, rows, K)
+    q.codes.copy_(torch.from_numpy(r.randint(0, 256, (rows, K // 2)).astype(np.uint8)))
+    lo, hi = (90, 160) if fmt == bb.MX_E8M0 else (0, 127)
+    q.scales.copy_(torch.from_numpy(r.randint(lo, hi, q.scales.numel()).astype(np.uint8)))
+    if fmt == bb.MX_E4M3:
+        q.row_scale.copy_(torch.from_numpy(2.0 ** r.randint(-30, 30, rows)).float())
+    out = torch.zeros(rows, K + 8, dtype=dtype, device="cuda")
+    bb.mx_dequant(q, out=out[:, :K])
+    assert np.array_equal(f64(out)[:, :K], values_of(q, [0, rows]))
+    assert not out[:, K:].any()
+
+
+def check_product(Y, X, W, x_starts, groups, y0=None):
+    """Y against the 64-bit product of the values that X and W stand for."""
+    xv = values_of(X, x_starts)
+    N = W.rows // groups
+    wv = values_of(W, list(range(0, W.rows + 1, N)))
+    Yh = f64(Y)
+    K = X.K
+    for e in range(groups):
+        a, b = x_starts[e], x_starts[e + 1]
+        w = wv[e * N:(e + 1) * N]
+        ref = xv[a:b] @ w.T
+        bound = (K / 64 + 8) * 2.0 ** -23 * (np.abs(xv[a:b]) @ np.abs(w).T) + 1e-35
+        if Y.dtype == torch.bfloat16:
+            bound = bound * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)
+        err = np.abs(Yh[a:b] - ref)
+        assert np.all(err <= bound), (e, float((err / bound).max()))
+    if y0 is not None:
+        outside = list(range(0, x_starts[0])) + list(range(x_starts[-1], Y.shape[0]))
+        assert (Yh[outside] == y0).all()
+    assert bb.device_timeouts() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("K", [32, 64, 96, 256, 288, 1056])
+def test_linear_one_tile(fmt, K):
+    """K inside one MMA step, one stage, and a last stage that is partly filled."""
+    X = bb.mx_quantize(activations(32, K, K).cuda(), fmt)
+    W = bb.mx_quantize(activations(128, K, K + 1).cuda(), fmt)
+    Y = bb.mx_linear(X, W)
+    torch.cuda.synchronize()
+    check_product(Y, X, W, [0, 32], 1)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [1, 2, 17, 33, 64, 65, 100, 128, 129, 200, 256, 300, 700])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_linear_tokens(fmt, M, out_dtype):
+    """Every token tile, partial tiles of both operands, split and unsplit K."""
+    N, K = 330, 2144
+    x = activations(M, K, M + 5)
+    X = bb.mx_quantize(x.cuda(), fmt)
+    W = bb.mx_quantize(synth.make_weight(N, K, 6).cuda(), fmt)
+    Y = bb.mx_linear(X, W, out_dtype=out_dtype)
+    torch.cuda.synchronize()
+    check_product(Y, X, W, [0, M], 1)
+    # the one-call form: the same bits, twice
+    for _ in range(2):
+        assert torch.equal(bb.mx_linear(x.cuda(), W, out_dtype=out_dtype), Y)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_linear_many_tiles(fmt):
+    """More tiles than SMs: persistent CTAs over several tiles, an accumulator reused."""
+    for M, N, K in ((30, 128 * 151, 320), (515, 128 * 100 + 7, 320), (1300, 3700, 544)):
+        X = bb.mx_quantize(activations(M, K, M).cuda(), fmt)
+        W = bb.mx_quantize(synth.make_weight(N, K, N).cuda(), fmt)
+        Y = bb.mx_linear(X, W)
+        torch.cuda.synchronize()
+        check_product(Y, X, W, [0, M], 1)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_linear_into_slices(fmt):
+    """Outputs side by side in one matrix, at odd columns, and fp32 activations."""
+    K, M, widths = 512, 50, (70, 33, 129)
+    x = activations(M, K, 2, torch.float32).cuda()
+    Ws = [bb.mx_quantize(synth.make_weight(n, K, n).cuda(), fmt) for n in widths]
+    for dtype in (torch.float32, torch.bfloat16):
+        y = torch.full((M, sum(widths) + 3), 5.0, dtype=dtype, device="cuda")
+        at = 1
+        for n, W in zip(widths, Ws):
+            bb.mx_linear(x, W, out=y[:, at:at + n])
+            at += n
+        X = bb.mx_quantize(x, fmt)
+        at = 1
+        for n, W in zip(widths, Ws):
+            check_product(y[:, at:at + n], X, W, [0, M], 1)
+            at += n
+        assert (y[:, 0] == 5.0).all() and (y[:, at:] == 5.0).all()
+
+
+GROUPS = [
+    [0, 5],                                # one group, ragged by offsets
+    [2, 2, 3, 40, 40, 41, 200],            # empty and single rows, rows of no group in front
+    [0, 0, 0, 0],                          # nothing at all
+    [0, 300, 300, 301, 700],               # tiles that start inside a scale band
+    [0] + [7 * i for i in range(1, 41)],   # many small groups
+    [0, 20, 20, 60, 61, 61, 61, 61, 61],   # few rows a group on average, one of 40
+    [0] * 30 + [150],                      # one group with all the rows
+]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("case", range(len(GROUPS)))
+@pytest.mark.parametrize("K", [96, 1184])
+def test_linear_grouped(fmt, case, K):
+    offsets = GROUPS[case]
+    E, N = len(offsets) - 1, 150
+    R = offsets[-1] + 3
+    x = activations(R, K, case + K)
+    off = torch.tensor(offsets, dtype=torch.int32).cuda()
+    X = bb.mx_quantize(x.cuda(), fmt, groups=E, offsets=off)
+    W = bb.mx_quantize(synth.make_weight(E * N, K, E).cuda(), fmt, groups=E)
+    for dtype in (torch.float32, torch.bfloat16):
+        Y = torch.full((R, N), 3.0, dtype=dtype, device="cuda")
+        bb.mx_linear(X, W, out=Y)
+        torch.cuda.synchronize()
+        check_product(Y, X, W, offsets, E, y0=3.0)
+        Y2 = torch.full((R, N), 3.0, dtype=dtype, device="cuda")
+        bb.mx_linear(x.cuda(), W, out=Y2, offsets=off)
+        assert torch.equal(Y, Y2)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_linear_equal_groups(fmt):
+    """Groups of equal size without offsets; expert weights of whole and partial tiles."""
+    for E, per, N in ((4, 35, 256), (3, 130, 100)):
+        K = 320
+        X = bb.mx_quantize(activations(E * per, K, E).cuda(), fmt, groups=E)
+        W = bb.mx_quantize(synth.make_weight(E * N, K, 8).cuda(), fmt, groups=E)
+        Y = bb.mx_linear(X, W)
+        torch.cuda.synchronize()
+        check_product(Y, X, W, [e * per for e in range(E + 1)], E)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_group_rows_do_not_depend_on_their_batch(fmt):
+    """A token's output is the same alone, in a batch and next to other experts'
+    rows: the same quantisation, and the same order of the sum where the plan
+    does not split K (many tiles)."""
+    K, N, E = 352, 128 * 40, 4
+    x = activations(64, K, 1).cuda()
+    W = bb.mx_quantize(synth.make_weight(E * N, K, 2).cuda(), fmt, groups=E)
+    off = torch.tensor([0, 16, 16, 40, 64], dtype=torch.int32).cuda()
+    Y = bb.mx_linear(x, W, offsets=off)
+    perm = torch.cat([torch.arange(16), torch.arange(16, 40).flip(0), torch.arange(40, 64)])
+    Z = bb.mx_linear(x, W, rows=perm.to(torch.int32).cuda(), offsets=off)
+    assert torch.equal(Z, Y[perm.cuda()])
+
+
+def test_empty_calls():
+    for fmt in FMTS:
+        W = bb.mx_quantize(synth.make_weight(40, 64, 1).cuda(), fmt)
+        x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+        X = bb.mx_quantize(x, fmt)
+        assert bb.mx_dequant(X).shape == (0, 64)
+        assert bb.mx_linear(X, W).shape == (0, 40) and bb.mx_linear(x, W).shape == (0, 40)
+        # rows that all come from padding
+        none = torch.full((5,), -1, dtype=torch.int32, device="cuda")
+        assert not bb.mx_linear(x, W, rows=none).any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_mixture_of_experts_block(fmt):
+    """The calls together, as a mixture-of-experts MLP uses them: rows gathered
+    by expert into the gate and up halves, SwiGLU and quantisation in one, the
+    down projection, and the weighted sum back to the tokens; each stage
+    against 64 bits on the values it was given."""
+    T, H, F, E, top = 45, 256, 224, 6, 2
+    g = torch.Generator().manual_seed(5)
+    x = activations(T, H, 3)
+    scores = torch.randn(T, E, generator=g)
+    scores[:, 4] = -9.0  # an expert that nobody picks
+    weight, pick = torch.softmax(scores, 1).topk(top, dim=1)
+    flat = pick.reshape(-1)
+    order = torch.sort(flat, stable=True).indices
+    rows = (order // top).to(torch.int32).cuda()
+    counts = torch.bincount(flat, minlength=E)
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)])
+    off = offsets.to(torch.int32).cuda()
+    up = bb.mx_quantize(synth.make_weight(E * 2 * F, H, 6).cuda(), fmt, groups=E)
+    down = bb.mx_quantize(synth.make_weight(E * H, F, 7).cuda(), fmt, groups=E)
+    hidden = bb.mx_linear(x.cuda(), up, rows=rows, offsets=off)
+    y = bb.mx_linear(hidden, down, offsets=off, swiglu=True)
+    out = torch.zeros(T, H, device="cuda").index_add_(
+        0, rows.long(), y * weight.reshape(-1)[order].cuda()[:, None])
+    torch.cuda.synchronize()
+    starts = offsets.tolist()
+    X = bb.mx_quantize(x.cuda(), fmt, rows=rows, groups=E, offsets=off)
+    check_product(hidden, X, up, starts, E)
+    Hq = bb.mx_quantize(hidden, fmt, swiglu=True, groups=E, offsets=off)
+    check_product(y, Hq, down, starts, E)
+    ref = np.zeros((T, H))
+    np.add.at(ref, rows.cpu().numpy(), f64(y) * f64(weight.reshape(-1)[order])[:, None])
+    # `top` products and sums in fp32
+    assert np.abs(f64(out) - ref).max() <= (top + 1) * 2.0 ** -23 * np.abs(f64(y)).max()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_streams_and_graphs(fmt):
+    """Two streams with a workspace each, and a captured call replayed on new
+    inputs and new expert counts."""
+    K, N, E, R = 512, 300, 3, 60
+    W = bb.mx_quantize(synth.make_weight(E * N, K, 2).cuda(), fmt, groups=E)
+    xs = [activations(R, K, s).cuda() for s in (1, 2)]
+    offs = [torch.tensor(o, dtype=torch.int32).cuda() for o in ([0, 20, 20, 60], [0, 1, 50, 58])]
+    want = [torch.zeros(R, N, device="cuda") for _ in xs]
+    for x, o, y in zip(xs, offs, want):
+        bb.mx_linear(x, W, offsets=o, out=y)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [torch.zeros(R, N, device="cuda") for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, x, o, y in zip(streams, xs, offs, got):
+            bb.mx_linear(x, W, offsets=o, out=y, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    x, o, y = xs[0].clone(), offs[0].clone(), torch.zeros(R, N, device="cuda")
+    ws = torch.empty(bb.mx_workspace_size(fmt, R, K, E), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        bb.mx_linear(x, W, offsets=o, out=y, ws=ws)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        bb.mx_linear(x, W, offsets=o, out=y, ws=ws)
+    launches = bb.kernel_launches()
+    for i in (1, 0, 1):
+        x.copy_(xs[i])
+        o.copy_(offs[i])
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i])
+    assert bb.kernel_launches() == launches

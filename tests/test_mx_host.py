@@ -1,0 +1,196 @@
+"""Host-side checks of the microscaled calls (no GPU): sizes, plans, and the
+refusals, which all come before anything is launched."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import _mx
+from activation_aware_codebook_b200 import binding as bb
+from activation_aware_codebook_b200.csrc import build as cbuild
+
+OK, INVALID, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3, 4, 6
+FAKE = 1 << 20  # an aligned address that is never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    cbuild.build()
+    return bb.load()
+
+
+def tensor(**kw):
+    d = dict(fmt=bb.MX_E4M3, groups=1, rows=64, K=256, codes=FAKE, scales=FAKE, row_scale=FAKE,
+             offsets=None)
+    d.update(kw)
+    return bb.CMxTensor(**d)
+
+
+def source(**kw):
+    d = dict(X=FAKE, type=0, flags=0, rows=64, ldx=256, index=None)
+    d.update(kw)
+    return bb.CMxSource(**d)
+
+
+def ref(x):
+    return ctypes.byref(x) if x is not None else None
+
+
+def test_struct_layouts():
+    assert ctypes.sizeof(bb.CMxTensor) == 56
+    assert ctypes.sizeof(bb.CMxSource) == 40
+
+
+@pytest.mark.parametrize("fmt", [bb.MX_E8M0, bb.MX_E4M3])
+@pytest.mark.parametrize("rows,K,groups", [(0, 32, 1), (1, 32, 1), (127, 96, 3), (128, 4096, 1),
+                                           (1000, 160, 64)])
+def test_sizes(lib, fmt, rows, K, groups):
+    n = bb.mx_scale_bytes(fmt, rows, K, groups)
+    assert n == _mx.scale_bytes(rows, K, fmt, groups)
+    # every scale of any split into groups has a place of its own inside
+    r = np.random.RandomState(rows + K)
+    for _ in range(5):
+        starts = np.sort(r.randint(0, rows + 1, groups + 1)).tolist()
+        at = _mx.scale_index(rows, K // _mx.BLOCK[fmt], starts)
+        used = at[at >= 0]
+        assert len(np.unique(used)) == len(used) and (len(used) == 0 or used.max() < n)
+    assert bb.mx_workspace_size(fmt, rows, K, groups) >= rows * K // 2 + n + 4 * rows
+
+
+def test_sizes_of_invalid_shapes(lib):
+    for args in ((2, 4, 64, 1), (0, -1, 64, 1), (0, 1 << 31, 64, 1), (0, 4, 48, 1), (0, 4, 0, 1),
+                 (0, 4, 64, 0), (0, 4, 64, 1025), (0, 4, 1 << 25, 1)):
+        assert bb.mx_scale_bytes(*args) == 0 and bb.mx_workspace_size(*args) == 0
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(fmt=2), UNSUPPORTED), (dict(rows=-1), SHAPE), (dict(K=272), SHAPE), (dict(K=0), SHAPE),
+    (dict(groups=0), SHAPE), (dict(groups=1025), SHAPE), (dict(groups=3), SHAPE),
+    (dict(codes=None), INVALID), (dict(codes=FAKE + 8), ALIGN), (dict(scales=None), INVALID),
+    (dict(scales=FAKE + 4), ALIGN), (dict(row_scale=None), INVALID),
+    (dict(row_scale=FAKE + 2), ALIGN), (dict(offsets=FAKE + 1), ALIGN)])
+def test_bad_tensors_are_refused(lib, kw, status):
+    t, good, src = tensor(**kw), tensor(), source()
+    assert lib.aaac_mx_quantize(ref(src), ref(t), None) == status
+    assert lib.aaac_last_error()
+    assert lib.aaac_mx_dequant(ref(t), FAKE, 1, 256, None) == status
+    assert lib.aaac_mx_linear(ref(t), ref(good), FAKE, 1, 64, None) == status
+    assert lib.aaac_mx_linear(ref(good), ref(t), FAKE, 1, 1 << 20, None) == status
+    assert lib.aaac_mx_linear_ws(ref(src), 64, None, ref(t), FAKE, 1, 1 << 20, FAKE, 1 << 40,
+                                 None) == status
+
+
+def test_null_tensors_are_refused(lib):
+    t, src = tensor(), source()
+    assert lib.aaac_mx_quantize(None, ref(t), None) == INVALID
+    assert lib.aaac_mx_quantize(ref(src), None, None) == INVALID
+    assert lib.aaac_mx_dequant(None, FAKE, 1, 256, None) == INVALID
+    assert lib.aaac_mx_linear(None, ref(t), FAKE, 1, 64, None) == INVALID
+    assert lib.aaac_mx_linear(ref(t), None, FAKE, 1, 64, None) == INVALID
+    assert lib.aaac_mx_linear_ws(None, 64, None, ref(t), FAKE, 1, 64, FAKE, 1 << 40, None) == INVALID
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(X=None), INVALID), (dict(X=FAKE + 8), ALIGN), (dict(type=2), UNSUPPORTED),
+    (dict(flags=2), INVALID), (dict(rows=63), SHAPE), (dict(rows=-1), SHAPE),
+    (dict(ldx=255), SHAPE), (dict(ldx=260), ALIGN), (dict(type=1, ldx=258), ALIGN),
+    (dict(flags=1), SHAPE), (dict(flags=1, ldx=511), SHAPE), (dict(index=FAKE + 2), ALIGN),
+    (dict(ldx=(1 << 31) + 8), SHAPE)])
+def test_bad_sources_are_refused(lib, kw, status):
+    src, t = source(**kw), tensor()
+    assert lib.aaac_mx_quantize(ref(src), ref(t), None) == status
+    assert lib.aaac_mx_linear_ws(ref(src), 64, None, ref(t), FAKE, 1, 64, FAKE, 1 << 40,
+                                 None) == status
+
+
+def test_bad_products_are_refused(lib):
+    x, w = tensor(), tensor(rows=128)
+    f = lib.aaac_mx_linear
+    assert f(ref(tensor(fmt=bb.MX_E8M0)), ref(w), FAKE, 1, 128, None) == INVALID     # formats
+    assert f(ref(tensor(K=288)), ref(w), FAKE, 1, 128, None) == SHAPE                # K
+    assert f(ref(tensor(groups=2)), ref(w), FAKE, 1, 128, None) == SHAPE             # groups
+    assert f(ref(x), ref(tensor(offsets=FAKE)), FAKE, 1, 128, None) == INVALID       # ragged w
+    assert f(ref(x), ref(tensor(rows=0)), FAKE, 1, 128, None) == SHAPE               # no weights
+    assert f(ref(x), ref(w), None, 1, 128, None) == INVALID                          # output
+    assert f(ref(x), ref(w), FAKE + 2, 1, 128, None) == ALIGN
+    assert f(ref(x), ref(w), FAKE + 1, 0, 128, None) == ALIGN
+    assert f(ref(x), ref(w), FAKE, 2, 128, None) == UNSUPPORTED
+    assert f(ref(x), ref(w), FAKE, 1, 127, None) == SHAPE
+    big = tensor(rows=(1 << 31) - 1)
+    assert f(ref(big), ref(big), FAKE, 1, 1 << 31, None) == SHAPE                    # tiles
+    g = lib.aaac_mx_linear_ws
+    need = bb.mx_workspace_size(bb.MX_E4M3, 64, 256, 1)
+    src = source()
+    assert g(ref(src), 64, None, ref(w), FAKE, 1, 128, None, need, None) == WORKSPACE
+    assert g(ref(src), 64, None, ref(w), FAKE, 1, 128, FAKE, need - 1, None) == WORKSPACE
+    assert g(ref(src), 64, None, ref(w), FAKE, 1, 128, FAKE + 8, need, None) == ALIGN
+    assert g(ref(src), -1, None, ref(w), FAKE, 1, 128, FAKE, need, None) == SHAPE
+    assert g(ref(src), 64, FAKE + 2, ref(w), FAKE, 1, 128, FAKE, need, None) == ALIGN
+    w3 = tensor(rows=129, groups=3)
+    assert g(ref(src), 64, None, ref(w3), FAKE, 1, 128, FAKE, 1 << 40, None) == SHAPE
+    assert lib.aaac_mx_dequant(ref(x), FAKE + 8, 1, 256, None) == ALIGN
+    assert lib.aaac_mx_dequant(ref(x), FAKE, 0, 260, None) == ALIGN
+    assert lib.aaac_mx_dequant(ref(x), FAKE, 0, 255, None) == SHAPE
+
+
+def test_no_rows_is_no_work(lib):
+    x, w, src = tensor(rows=0, codes=None, scales=None, row_scale=None), tensor(), source(rows=0, X=None)
+    before = bb.kernel_launches()
+    assert lib.aaac_mx_quantize(ref(src), ref(x), None) == OK
+    assert lib.aaac_mx_dequant(ref(x), None, 1, 256, None) == OK
+    assert lib.aaac_mx_linear(ref(x), ref(w), None, 1, 64, None) == OK
+    assert lib.aaac_mx_linear_ws(ref(src), 0, None, ref(w), None, 1, 64, None, 0, None) == OK
+    assert bb.kernel_launches() == before
+
+
+def test_armed_fault_stops_every_call(lib):
+    x, w, src = tensor(), tensor(), source()
+    for call in (lambda: lib.aaac_mx_quantize(ref(src), ref(x), None),
+                 lambda: lib.aaac_mx_dequant(ref(x), FAKE, 1, 256, None),
+                 lambda: lib.aaac_mx_linear(ref(x), ref(w), FAKE, 1, 64, None),
+                 lambda: lib.aaac_mx_linear_ws(ref(src), 64, None, ref(w), FAKE, 1, 64, FAKE,
+                                               1 << 40, None)):
+        before = bb.kernel_launches()
+        bb.inject_fault("launch")
+        assert call() == 5
+        assert bb.kernel_launches() == before
+
+
+@pytest.mark.parametrize("groups,rows", [(1, 1), (1, 32), (1, 33), (1, 64), (1, 128), (1, 129),
+                                         (1, 8192), (8, 3), (64, 128), (16, 8200), (1024, 5)])
+@pytest.mark.parametrize("N,K", [(1, 32), (1024, 4096), (4096, 4096), (14336, 4096),
+                                 (5120, 27648), (100, 4096)])
+def test_plan_covers_every_split_of_the_rows(lib, groups, rows, N, K):
+    p = bb.mx_launch_plan(groups, rows, N, K)
+    assert p["stages"] == -(-K // 256)
+    assert 1 <= p["split"] <= min(8, p["stages"])
+    n_tiles = -(-N // 128)
+    assert p["columns"] in (32, 64, 128, 256)
+    # a 32-token tile may not start inside a scale band: one such tile a group
+    assert p["columns"] > 32 or (groups == 1 and rows <= 32)
+    r = np.random.RandomState(groups + rows)
+    for k in range(20):
+        cut = np.sort(r.randint(0, rows + 1, groups - 1))
+        if k == 0:
+            cut[:] = rows
+        counts = np.diff(np.concatenate([[0], cut, [rows]]))
+        tiles = int(sum(-(-c // p["columns"]) for c in counts)) * n_tiles
+        assert tiles <= p["tiles"]
+    if p["split"] > 1:  # a cluster a tile
+        assert p["ctas"] == p["tiles"] * p["split"]
+
+
+def test_plan_refusals(lib):
+    out = (ctypes.c_int32 * 5)()
+    assert lib.aaac_mx_launch_plan(1, 4, 4, 64, None) == INVALID
+    for args in ((0, 4, 4, 64), (1, 0, 4, 64), (1, 4, 0, 64), (1, 4, 4, 48),
+                 (1, (1 << 31) - 1, (1 << 31) - 1, 64)):
+        assert lib.aaac_mx_launch_plan(*args, out) == SHAPE
+
+
+def test_binding_refuses_without_cuda(lib):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    with pytest.raises(RuntimeError):
+        bb.mx_quantize(torch.zeros(8, 64, dtype=torch.bfloat16), bb.MX_E4M3)
