@@ -549,25 +549,30 @@ class MxTensor:
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor,
                  row_scale: Optional[torch.Tensor], fmt: int, groups: int = 1,
                  offsets: Optional[torch.Tensor] = None):
+        if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous():
+            raise ValueError("codes must be contiguous uint8 [rows, K/2]")
+        rows, half = codes.shape
+        need = _mx_bytes(load().aaac_mx_scale_bytes, fmt, rows, 2 * half, groups)
+        if scales.dtype != torch.uint8 or scales.numel() < need or not scales.is_contiguous():
+            raise ValueError(f"scales must be contiguous uint8, {need} bytes")
+        if fmt != MX_E4M3:
+            row_scale = None
+        elif (row_scale is None or row_scale.dtype != torch.float32 or row_scale.numel() < rows
+              or not row_scale.is_contiguous()):
+            raise ValueError(f"row_scale must be contiguous float32 [{rows}]")
+        if offsets is not None:
+            _mx_offsets(offsets, groups)
+        _mx_on(codes.get_device(), codes, scales, row_scale, offsets)
+        self._set(codes, scales, row_scale, fmt, groups, offsets, rows, 2 * half)
+
+    def _set(self, codes, scales, row_scale, fmt, groups, offsets, rows, K):
         self.codes, self.scales, self.row_scale = codes, scales, row_scale
         self.fmt, self.groups, self.offsets = fmt, groups, offsets
-        self.rows, self.K = codes.shape[0], 2 * codes.shape[1]
-        if codes.dtype != torch.uint8 or not codes.is_contiguous():
-            raise ValueError("codes must be contiguous uint8 [rows, K/2]")
-        need = mx_scale_bytes(fmt, self.rows, self.K, groups)
-        if scales.dtype != torch.uint8 or not scales.is_contiguous() or scales.numel() < need:
-            raise ValueError(f"scales must be contiguous uint8, {need} bytes")
-        if fmt == MX_E4M3 and (row_scale is None or row_scale.dtype != torch.float32
-                               or not row_scale.is_contiguous()
-                               or row_scale.numel() < self.rows):
-            raise ValueError(f"row_scale must be contiguous float32 [{self.rows}]")
-        _mx_offsets(offsets, groups)
-        same = [t for t in (scales, row_scale if fmt == MX_E4M3 else None, offsets)
-                if t is not None]
-        if any(t.device != codes.device for t in same):
-            raise ValueError("the parts of a microscaled tensor lie on different devices")
-        self._c = CMxTensor(fmt, groups, self.rows, self.K, _ptr(codes), _ptr(scales),
-                            _ptr(row_scale) if fmt == MX_E4M3 else None, _ptr(offsets))
+        self.rows, self.K = rows, K
+        self._c = CMxTensor(fmt, groups, rows, K, codes.data_ptr(), scales.data_ptr(),
+                            None if row_scale is None else row_scale.data_ptr(),
+                            None if offsets is None else offsets.data_ptr())
+        self._ref = ctypes.byref(self._c)
 
     @property
     def device(self):
@@ -576,34 +581,59 @@ class MxTensor:
     @staticmethod
     def empty(fmt: int, rows: int, K: int, groups: int = 1,
               offsets: Optional[torch.Tensor] = None, device="cuda") -> "MxTensor":
-        need = mx_scale_bytes(fmt, rows, K, groups)
-        if need == 0:
-            raise AaacError(2, load().aaac_last_error().decode())
-        return MxTensor(torch.empty(rows, K // 2, dtype=torch.uint8, device=device),
-                        torch.empty(need, dtype=torch.uint8, device=device),
-                        (torch.empty(rows, dtype=torch.float32, device=device)
-                         if fmt == MX_E4M3 else None), fmt, groups, offsets)
+        need = _mx_bytes(load().aaac_mx_scale_bytes, fmt, rows, K, groups)
+        if offsets is not None:
+            _mx_offsets(offsets, groups)
+        t = object.__new__(MxTensor)
+        codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=device)
+        scales = torch.empty(need, dtype=torch.uint8, device=device)
+        row_scale = (torch.empty(rows, dtype=torch.float32, device=device) if fmt == MX_E4M3
+                     else None)
+        t._set(codes, scales, row_scale, fmt, groups, offsets, rows, K)
+        return t
 
 
-def _mx_offsets(offsets: Optional[torch.Tensor], groups: int) -> None:
-    if offsets is not None and (offsets.dtype != torch.int32 or not offsets.is_contiguous()
-                                or offsets.numel() != groups + 1):
+def _mx_bytes(size, fmt: int, rows: int, K: int, groups: int) -> int:
+    """A size query's answer; its refusal (0) as the error it names."""
+    need = size(fmt, rows, K, groups)
+    if need == 0:
+        raise AaacError(2, load().aaac_last_error().decode())
+    return need
+
+
+def _mx_offsets(offsets: torch.Tensor, groups: int) -> None:
+    if (offsets.dtype != torch.int32 or offsets.numel() != groups + 1
+            or not offsets.is_contiguous()):
         raise ValueError(f"offsets must be contiguous int32 [{groups + 1}]")
 
 
-def _mx_on(device, *tensors) -> None:
-    """Every tensor on `device`, and that the current one: the library launches there."""
+def _mx_on(device: int, *tensors) -> None:
+    """Every tensor on CUDA device `device`."""
+    if device < 0:
+        raise ValueError("libaaac takes device tensors only")
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {t.device} and {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on device {t.get_device()} and device {device}")
 
 
-def _scope(stream):
-    """What a call allocates for itself belongs to the stream it runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _mx_stream(device: int, stream) -> int:
+    """The stream a call runs on.  The library launches on the current device,
+    so the tensors have to be there."""
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors on device {device}, but the current device is "
+                         f"{torch.cuda.current_device()}")
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _on_stream(f, stream, *args):
+    """f(*args), its own allocations made on `stream` (the caching allocator
+    ties memory to the stream it was allocated on)."""
+    if stream is None:
+        return f(*args)
+    with torch.cuda.stream(stream):
+        return f(*args)
 
 
 def _mx_source(X: torch.Tensor, rows: Optional[torch.Tensor], swiglu: bool):
@@ -614,26 +644,24 @@ def _mx_source(X: torch.Tensor, rows: Optional[torch.Tensor], swiglu: bool):
                              or not rows.is_contiguous()):
         raise ValueError("rows must be contiguous int32 [quantised rows]")
     n, width = X.shape
-    if (X.stride(1) != 1 or X.stride(0) * X.element_size() % 16 or X.stride(0) < width
-            or X.data_ptr() % 16):
+    ldx, step = X.stride()
+    if step != 1 or ldx * X.element_size() % 16 or ldx < width or X.data_ptr() % 16:
         X = X.contiguous()
-    src = CMxSource(_ptr(X), _MX_TYPES[X.dtype], MX_SWIGLU if swiglu else 0, n, X.stride(0),
-                    _ptr(rows))
+        ldx = width
+    src = CMxSource(X.data_ptr(), _MX_TYPES[X.dtype], MX_SWIGLU if swiglu else 0, n, ldx,
+                    None if rows is None else rows.data_ptr())
     return src, n if rows is None else rows.numel(), width // 2 if swiglu else width, X
 
 
-def _mx_out(out: Optional[torch.Tensor], rows: int, cols: int, dtype, device) -> torch.Tensor:
+def _mx_out(out: Optional[torch.Tensor], rows: int, cols: int, dtype, like: torch.Tensor):
+    """(output, its aaac_type, its leading dimension)."""
     if out is None:
-        return torch.empty(rows, cols, dtype=dtype, device=device)
+        return torch.empty((rows, cols), dtype=dtype, device=like.device), _MX_TYPES[dtype], cols
     if (out.shape != (rows, cols) or out.dtype not in _MX_TYPES
             or (cols > 1 and out.stride(1) != 1)):
         raise ValueError(f"out must be a bfloat16 or float32 [{rows}, {cols}] with "
                          "consecutive columns")
-    return out
-
-
-def _ld(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return out, _MX_TYPES[out.dtype], out.stride(0) if rows > 1 else max(out.stride(0), cols)
 
 
 def mx_quantize(X: torch.Tensor, fmt: int, rows: Optional[torch.Tensor] = None,
@@ -645,16 +673,19 @@ def mx_quantize(X: torch.Tensor, fmt: int, rows: Optional[torch.Tensor] = None,
     swiglu quantises silu(a) * b of X's two halves [n, 2K]; groups and offsets
     are the rows' groups (see MxTensor)."""
     _need_cuda()
-    with _scope(stream):
-        src, n, K, X = _mx_source(X, rows, swiglu)
-        if out is None:
-            _mx_offsets(offsets, groups)
-            out = MxTensor.empty(fmt, n, K, groups, offsets, X.device)
-        elif (out.fmt, out.rows, out.K) != (fmt, n, K):
-            raise ValueError(f"out is fmt {out.fmt} [{out.rows}, {out.K}], not {fmt} [{n}, {K}]")
-        _mx_on(X.device, rows, out.codes)
-        _check(load().aaac_mx_quantize(ctypes.byref(src), ctypes.byref(out._c),
-                                       _stream(stream)))
+    return _on_stream(_mx_quantize, stream, X, fmt, rows, swiglu, groups, offsets, out, stream)
+
+
+def _mx_quantize(X, fmt, rows, swiglu, groups, offsets, out, stream):
+    src, n, K, X = _mx_source(X, rows, swiglu)
+    device = X.get_device()
+    at = _mx_stream(device, stream)
+    if out is None:
+        out = MxTensor.empty(fmt, n, K, groups, offsets, X.device)
+    elif (out.fmt, out.rows, out.K) != (fmt, n, K):
+        raise ValueError(f"out is fmt {out.fmt} [{out.rows}, {out.K}], not {fmt} [{n}, {K}]")
+    _mx_on(device, rows, out.codes, offsets)
+    _check(load().aaac_mx_quantize(ctypes.byref(src), out._ref, at))
     return out
 
 
@@ -662,11 +693,15 @@ def mx_dequant(q: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = 
                stream=None) -> torch.Tensor:
     """A microscaled tensor's values, bf16 or fp32 [rows, K]."""
     _need_cuda()
-    with _scope(stream):
-        out = _mx_out(out, q.rows, q.K, dtype, q.device)
-        _mx_on(q.device, out)
-        _check(load().aaac_mx_dequant(ctypes.byref(q._c), _ptr(out), _MX_TYPES[out.dtype],
-                                      _ld(out), _stream(stream)))
+    return _on_stream(_mx_dequant, stream, q, dtype, out, stream)
+
+
+def _mx_dequant(q, dtype, out, stream):
+    device = q.codes.get_device()
+    at = _mx_stream(device, stream)
+    out, kind, ld = _mx_out(out, q.rows, q.K, dtype, q.codes)
+    _mx_on(device, out)
+    _check(load().aaac_mx_dequant(q._ref, out.data_ptr(), kind, ld, at))
     return out
 
 
@@ -680,29 +715,40 @@ def mx_linear(X: Union[torch.Tensor, MxTensor], W: MxTensor, out: Optional[torch
     mx_quantize does (rows, swiglu and offsets as there; ws: a workspace of
     mx_workspace_size bytes)."""
     _need_cuda()
-    with _scope(stream):
-        N = W.rows // W.groups
-        if isinstance(X, MxTensor):
-            if rows is not None or swiglu or offsets is not None or ws is not None:
-                raise ValueError("rows, swiglu, offsets and ws go with activations that are "
-                                 "not quantised yet")
-            out = _mx_out(out, X.rows, N, out_dtype, X.device)
-            _mx_on(X.device, W.codes, out)
-            _check(load().aaac_mx_linear(ctypes.byref(X._c), ctypes.byref(W._c), _ptr(out),
-                                         _MX_TYPES[out.dtype], _ld(out), _stream(stream)))
-            return out
-        src, n, K, X = _mx_source(X, rows, swiglu)
-        if K != W.K:
-            raise ValueError(f"X has K={K}, W has K={W.K}")
+    if isinstance(X, MxTensor):
+        if rows is not None or swiglu or offsets is not None or ws is not None:
+            raise ValueError("rows, swiglu, offsets and ws go with activations that are not "
+                             "quantised yet")
+        return _on_stream(_mx_product, stream, X, W, out, out_dtype, stream)
+    return _on_stream(_mx_linear, stream, X, W, out, out_dtype, rows, swiglu, offsets, ws, stream)
+
+
+def _mx_product(X, W, out, out_dtype, stream):
+    device = X.codes.get_device()
+    at = _mx_stream(device, stream)
+    out, kind, ld = _mx_out(out, X.rows, W.rows // W.groups, out_dtype, X.codes)
+    _mx_on(device, W.codes, out)
+    _check(load().aaac_mx_linear(X._ref, W._ref, out.data_ptr(), kind, ld, at))
+    return out
+
+
+def _mx_linear(X, W, out, out_dtype, rows, swiglu, offsets, ws, stream):
+    src, n, K, X = _mx_source(X, rows, swiglu)
+    device = X.get_device()
+    at = _mx_stream(device, stream)
+    if K != W.K:
+        raise ValueError(f"X has K={K}, W has K={W.K}")
+    if offsets is not None:
         _mx_offsets(offsets, W.groups)
-        out = _mx_out(out, n, N, out_dtype, X.device)
-        if ws is None:
-            ws = torch.empty(mx_workspace_size(W.fmt, n, K, W.groups), dtype=torch.uint8,
-                             device=X.device)
-        _mx_on(X.device, rows, offsets, W.codes, out, ws)
-        _check(load().aaac_mx_linear_ws(ctypes.byref(src), n, _ptr(offsets), ctypes.byref(W._c),
-                                        _ptr(out), _MX_TYPES[out.dtype], _ld(out), _ptr(ws),
-                                        ws.numel(), _stream(stream)))
+    out, kind, ld = _mx_out(out, n, W.rows // W.groups, out_dtype, X)
+    if ws is None:
+        need = _mx_bytes(load().aaac_mx_workspace_size, W.fmt, n, K, W.groups)
+        ws = torch.empty(need, dtype=torch.uint8, device=X.device)
+    _mx_on(device, rows, offsets, W.codes, out, ws)
+    _check(load().aaac_mx_linear_ws(ctypes.byref(src), n,
+                                    None if offsets is None else offsets.data_ptr(), W._ref,
+                                    out.data_ptr(), kind, ld, ws.data_ptr(),
+                                    ws.numel() * ws.element_size(), at))
     return out
 
 

@@ -9,12 +9,13 @@
 // narrow MMA and not a 128-row tile of padding, and a warp's 32 lanes hold 32
 // consecutive n of one token when Y is stored.  Per stage of 256 columns of K
 // (one 128-byte swizzle row of packed codes per operand row):
-//   warp 0      one lane issues the TMA copies of both code tiles
-//               (SWIZZLE_128B) and the bulk copies of their scale tiles;
-//   warp 1      one lane copies the scale tiles to tensor memory
-//               (tcgen05.cp 32x128b, one per 512-byte tile) and issues four
-//               MMAs of K = 64; copies and MMAs of one thread run in order;
-//   warps 2..9  epilogue: tensor memory -> registers, the accumulator handed
+//   warp 0      one lane issues four TMA copies: both code tiles
+//               (SWIZZLE_128B) and both operands' scale tiles;
+//   warps 2..5  bring the scale tiles from shared to tensor memory, one lane
+//               quadrant each (the tensor core wants a copy in all four), two
+//               stages in turn;
+//   warp 1      one lane issues four MMAs of K = 64;
+//   the others  epilogue: tensor memory -> registers, the accumulator handed
 //               back, row scales, stores.
 // The tensor core's N is the tile's own row count rounded up to 16, so a
 // ragged tile costs what its rows cost.
@@ -38,15 +39,12 @@ constexpr int kWRows = 128;        // weight rows of a tile (MMA M)
 constexpr int kStageK = 256;       // columns of a stage
 constexpr int kRowBytes = 128;     // of packed codes per stage and row
 constexpr int kSteps = 4;          // MMAs of K = 64 per stage
-constexpr int kEpiWarps = 8;
-constexpr int kMxThreads = (2 + kEpiWarps) * 32;
+constexpr int kEpiWarp = 6;        // the first epilogue warp
 constexpr int kWTile = kWRows * kRowBytes;  // 16 KB
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kSms = 148;
 
 struct MxGemmArgs {
-  const uint8_t* sx;
-  const uint8_t* sw;
   const float* gx;
   const float* gw;
   void* Y;
@@ -55,7 +53,7 @@ struct MxGemmArgs {
   int N, K;
   int n_tiles;        // 128-row weight tiles per group
   int stages;         // ceil(K / 256)
-  int tiles_k;        // scale tiles along K
+  int box;            // token rows of one TMA copy
   int bf16_out;
 };
 
@@ -65,30 +63,28 @@ struct Shape {
   static constexpr int kAtoms = FMT == kMxE8m0 ? 2 : 4;     // scale tiles of a stage along K
   static constexpr int kScale = kAtoms * kMxTileBytes;      // of one band
   static constexpr int kXTile = NT * kRowBytes;
-  static constexpr int kBox = NT < 128 ? 32 : 64;           // token rows of one TMA copy
   static constexpr int kStage = kWTile + kXTile + kScale * (1 + kSub);
+  // 64 columns an epilogue thread at most: all of them leave tensor memory in
+  // one go, so that the next tile's MMAs wait for no store
+  static constexpr int kEpiWarps = NT == 256 ? 16 : 8;
+  static constexpr int kThreads = (kEpiWarp + kEpiWarps) * 32;
   static constexpr int kStages = NT == 256 ? 4 : (NT == 128 ? 6 : (NT == 64 ? 7 : 8));
-  static constexpr int kSmem = 1024 + kStages * kStage + (2 * kStages + 4) * 8 + 16;
-  static_assert(kSmem + 4 * (kMxMaxGroups + 1) + 64 <= kSmemLimit, "shared memory");
+  static constexpr int kSmem = 1024 + kStages * kStage + (2 * kStages + 6) * 8 + 16;
+  static_assert(kSmem + 4 * (kMxMaxGroups + 1) + 16 * NT + 64 <= kSmemLimit, "shared memory");
 };
 
 template <int NT, bool SPLIT>
 struct Tmem {
   static constexpr int kBufs = SPLIT || NT == 256 ? 1 : 2;  // accumulators
-  static constexpr int kScaleX = kBufs * NT;                // columns: scales of X, then of W
-  static constexpr int kScaleW = kScaleX + 16 * ((NT + 127) / 128);
-  static constexpr int kUsed = kScaleW + 16;
+  static constexpr int kScale = kBufs * NT;                 // first scale column
+  static constexpr int kScaleX = 16 * ((NT + 127) / 128);   // of a stage: X's columns, then 16 of W
+  static constexpr int kUsed = kScale + 2 * (kScaleX + 16); // two stages in turn
   static constexpr int kCols = kUsed <= 64 ? 64 : (kUsed <= 128 ? 128 : (kUsed <= 256 ? 256 : 512));
 };
 
-// Descriptor of one scale tile for tcgen05.cp: no swizzle, 8-row groups of 16
-// bytes a row 128 bytes apart (SBO = 8 x 16 B), descriptor version 1.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3fffu) | ((uint64_t)8 << 32) | ((uint64_t)1 << 46);
-}
-__device__ __forceinline__ void scale_copy(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-               : "memory");
+// sw128_desc of a code tile whose address is given in 16-byte units.
+__device__ __forceinline__ uint64_t code_desc(uint32_t at) {
+  return (uint64_t)(at | 1u << 16) | ((uint64_t)(64u | 1u << 14 | 2u << 29) << 32);
 }
 
 // Instruction descriptor of the block-scaled kinds: A and B E2M1 (bits 7-9 and
@@ -96,10 +92,9 @@ __device__ __forceinline__ void scale_copy(uint32_t taddr, uint64_t desc) {
 // UE4M3), M >> 7 at bit 27; the scale words' byte offsets of B at bit 4 and of
 // A at bit 29.
 template <int FMT>
-__device__ __forceinline__ uint32_t mx_idesc(int N, int sf_id) {
+__device__ __forceinline__ uint32_t mx_idesc(int N) {
   return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
-         ((FMT == kMxE8m0 ? 1u : 0u) << 23) | (1u << 27) | ((uint32_t)sf_id << 4) |
-         ((uint32_t)sf_id << 29);
+         ((FMT == kMxE8m0 ? 1u : 0u) << 23) | (1u << 27);
 }
 
 template <int FMT>
@@ -121,13 +116,25 @@ __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t adesc, uint64_t bdes
         : "memory");
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
+// N consecutive columns of this warp's lane quadrant, from registers.
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
+  static_assert(N == 8 || N == 16 || N == 32, "columns");
+  if (N == 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::
+                     "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+                 "r"(r[6]), "r"(r[7])
+                 : "memory");
+  else
+#pragma unroll
+    for (int i = 0; i < N; i += 16)
+      asm volatile(
+          "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+          "%11, %12, %13, %14, %15, %16};" ::"r"(taddr + i),
+          "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]),
+          "r"(r[i + 6]), "r"(r[i + 7]), "r"(r[i + 8]), "r"(r[i + 9]), "r"(r[i + 10]),
+          "r"(r[i + 11]), "r"(r[i + 12]), "r"(r[i + 13]), "r"(r[i + 14]), "r"(r[i + 15])
+          : "memory");
 }
 
 // What a kernel launched to overlap the quantisation before it must not read
@@ -159,12 +166,12 @@ struct TileAt {
   int first;   // the group's first row
 };
 
-// Tile `item`; *e (the search's start) only moves forward.
+// Tile `item`, one of the s_pre[groups] * n_tiles; *e (the search's start) only
+// moves forward.
 template <int NT>
-__device__ __forceinline__ bool tile_at(const MxGemmArgs& a, const int* s_pre, int item, int* e,
+__device__ __forceinline__ void tile_at(const MxGemmArgs& a, const int* s_pre, int item, int* e,
                                         TileAt* t) {
-  while (*e < a.rows.groups && item >= s_pre[*e + 1] * a.n_tiles) (*e)++;
-  if (*e >= a.rows.groups) return false;
+  while (item >= s_pre[*e + 1] * a.n_tiles) (*e)++;
   const int tt = s_pre[*e + 1] - s_pre[*e];
   const int at = item - s_pre[*e] * a.n_tiles;
   int last;
@@ -174,32 +181,12 @@ __device__ __forceinline__ bool tile_at(const MxGemmArgs& a, const int* s_pre, i
   t->local = (at % tt) * NT;
   t->row = t->first + t->local;
   t->count = min(NT, last - t->row);
-  return true;
 }
 
-// One step of the producer's walk over (tile, stage).
-template <int NT>
-struct Walk {
-  const MxGemmArgs& a;
-  const int* s_pre;
-  int item, step, lo, hi, st, e;
-  TileAt t;
-  bool valid;
-  __device__ Walk(const MxGemmArgs& a_, const int* p, int item_, int step_, int lo_, int hi_)
-      : a(a_), s_pre(p), item(item_), step(step_), lo(lo_), hi(hi_), st(lo_), e(0) {
-    valid = tile_at<NT>(a, s_pre, item, &e, &t);
-  }
-  __device__ void next() {
-    if (++st < hi) return;
-    st = lo;
-    item += step;
-    valid = step > 0 && tile_at<NT>(a, s_pre, item, &e, &t);
-  }
-};
-
 template <int FMT, int NT, bool SPLIT>
-__global__ void __launch_bounds__(kMxThreads, 1)
+__global__ void __launch_bounds__((Shape<FMT, NT>::kThreads), 1)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+               const __grid_constant__ CUtensorMap sxmap, const __grid_constant__ CUtensorMap swmap,
                const __grid_constant__ MxGemmArgs a) {
   using S = Shape<FMT, NT>;
   using TM = Tmem<NT, SPLIT>;
@@ -214,12 +201,14 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   uint64_t* empty = full + S::kStages;
   uint64_t* acc_full = empty + S::kStages;  // [2]
   uint64_t* acc_empty = acc_full + 2;       // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* scale_full = acc_empty + 2;     // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scale_full + 2);
   __shared__ int s_pre[kMxMaxGroups + 1];  // token tiles of the groups before
+  __shared__ __align__(16) float s_gx[S::kEpiWarps][FMT == kMxE4m3 && !SPLIT ? NT / (S::kEpiWarps / 4) : 4];
   __shared__ int s_fail;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < a.rows.groups; e += kMxThreads) {
+  for (int e = threadIdx.x; e < a.rows.groups; e += S::kThreads) {
     int first, last;
     mx_group(a.rows, e, &first, &last);
     s_pre[e + 1] = (last - first + NT - 1) / NT;
@@ -230,8 +219,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       mbar_init(&empty[s], 1);  // MMA commit
     }
     for (int b = 0; b < 2; b++) {
-      mbar_init(&acc_full[b], 1);           // MMA commit of a tile
-      mbar_init(&acc_empty[b], kEpiWarps);  // one arrive per epilogue warp
+      mbar_init(&acc_full[b], 1);              // MMA commit of a tile
+      mbar_init(&acc_empty[b], S::kEpiWarps);  // one arrive per epilogue warp
+      mbar_init(&scale_full[b], 4);            // one arrive per scale warp
     }
     s_fail = 0;
     s_pre[0] = 0;
@@ -272,44 +262,63 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   const int st_lo = SPLIT ? (int)((int64_t)crank * a.stages / csize) : 0;
   const int st_hi = SPLIT ? (int)((int64_t)(crank + 1) * a.stages / csize) : a.stages;
 
+  const int nst = st_hi - st_lo;
+  const int items = s_pre[a.rows.groups] * a.n_tiles;
+
   if (warp == 0) {
     if (lane == 0) {
-      auto atoms = [&](int st) { return min(S::kAtoms, a.tiles_k - st * S::kAtoms); };
-      auto bands = [&](const TileAt& t) { return (t.count + 127) / 128; };
-      auto boxes = [&](const TileAt& t) { return (t.count + S::kBox - 1) / S::kBox; };
-      auto load_w = [&](const Walk<NT>& w, int s) {
-        const uint32_t sb = (uint32_t)(atoms(w.st) * kMxTileBytes);
-        mbar_arrive_expect_tx(&full[s],
-                              kWTile + boxes(w.t) * S::kBox * kRowBytes + sb * (1 + bands(w.t)));
-        tma_load_2d(sW + s * kWTile, &wmap, &full[s], w.st * kRowBytes, w.t.e * a.N + w.t.n0);
-        const int64_t band = (int64_t)w.t.e * a.N / kMxTileRows + w.t.e + w.t.n0 / kMxTileRows;
-        bulk_load(sSW + s * S::kScale,
-                  a.sw + (band * a.tiles_k + w.st * S::kAtoms) * kMxTileBytes, sb, &full[s]);
+      // coordinates of a tile's copies: the rows of the codes and the bands of
+      // the scales, of both operands
+      struct At {
+        int w, sw, x, sx, boxes;
       };
-      auto load_x = [&](const Walk<NT>& w, int s) {
-        for (int j = 0; j < boxes(w.t); j++)  // only boxes that hold rows of the tile
-          tma_load_2d(sX + s * S::kXTile + j * S::kBox * kRowBytes, &xmap, &full[s],
-                      w.st * kRowBytes, w.t.row + j * S::kBox);
-        const uint32_t sb = (uint32_t)(atoms(w.st) * kMxTileBytes);
-        const int64_t band = w.t.first / kMxTileRows + w.t.e + w.t.local / kMxTileRows;
-        for (int j = 0; j < bands(w.t); j++)
-          bulk_load(sSX + (s * S::kSub + j) * S::kScale,
-                    a.sx + ((band + j) * a.tiles_k + w.st * S::kAtoms) * kMxTileBytes, sb,
-                    &full[s]);
+      auto at_of = [&](const TileAt& t) {
+        At c;
+        c.w = t.e * a.N + t.n0;
+        c.sw = (int)((int64_t)t.e * a.N / kMxTileRows) + t.e + t.n0 / kMxTileRows;
+        c.x = t.row;
+        c.sx = t.first / kMxTileRows + t.e + t.local / kMxTileRows;
+        c.boxes = (t.count + a.box - 1) / a.box;  // only boxes that hold rows of the tile
+        return c;
       };
-      // the first stages' weights do not wait for X
+      const uint32_t box_bytes = (uint32_t)(a.box * kRowBytes);
+      auto load_w = [&](const At& c, int st, int s) {
+        mbar_arrive_expect_tx(&full[s], kWTile + c.boxes * box_bytes + S::kScale * (1 + S::kSub));
+        tma_load_2d(sW + s * kWTile, &wmap, &full[s], st * kRowBytes, c.w);
+        tma_load_2d(sSW + s * S::kScale, &swmap, &full[s], st * (S::kScale / 8), c.sw);
+      };
+      auto load_x = [&](const At& c, int st, int s) {
+        for (int j = 0; j < c.boxes; j++)
+          tma_load_2d(sX + s * S::kXTile + j * box_bytes, &xmap, &full[s], st * kRowBytes,
+                      c.x + j * a.box);
+        tma_load_2d(sSX + s * S::kSub * S::kScale, &sxmap, &full[s], st * (S::kScale / 8), c.sx);
+      };
+      TileAt t;
+      int e = 0;
+      // the first tile's first stages: their weights do not wait for X
       int ahead = 0;
-      for (Walk<NT> w(a, s_pre, item0, step, st_lo, st_hi); w.valid && ahead < S::kStages; w.next())
-        load_w(w, ahead++);
+      if (item0 < items) {
+        tile_at<NT>(a, s_pre, item0, &e, &t);
+        const At c = at_of(t);
+        for (; ahead < min(nst, S::kStages); ahead++) load_w(c, st_lo + ahead, ahead);
+      }
       wait_for_x();
       int it = 0;
-      for (Walk<NT> w(a, s_pre, item0, step, st_lo, st_hi); w.valid && !s_fail; w.next(), it++) {
-        const int s = it % S::kStages;
-        if (it >= ahead) {
-          if (!mbar_wait(&empty[s], ((it / S::kStages) - 1) & 1)) { s_fail = 1; break; }
-          load_w(w, s);
+      for (int item = item0; item < items && !s_fail; item += step) {
+        tile_at<NT>(a, s_pre, item, &e, &t);
+        const At c = at_of(t);
+        for (int st = st_lo; st < st_hi; st++, it++) {
+          const int s = it % S::kStages;
+          if (it >= ahead) {
+            if (it >= S::kStages && !mbar_wait(&empty[s], ((it / S::kStages) - 1) & 1)) {
+              s_fail = 1;
+              break;
+            }
+            load_w(c, st, s);
+          }
+          load_x(c, st, s);
         }
-        load_x(w, s);
+        if (SPLIT) break;
       }
       // the last copies have landed before the CTA can exit (bounded)
       for (int j = it > S::kStages ? it - S::kStages : 0; j < it; j++)
@@ -318,9 +327,12 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   } else if (warp == 1) {
     if (lane == 0) {
       const int steps_all = (a.K + 63) / 64;
+      // addresses in 16-byte units, as descriptors hold them
+      const uint32_t w_lo = smem_u32(sW) >> 4, x_lo = smem_u32(sX) >> 4;
       TileAt t;
       int e = 0, it = 0, i = 0;
-      for (int item = item0; tile_at<NT>(a, s_pre, item, &e, &t) && !s_fail; item += step, i++) {
+      for (int item = item0; item < items && !s_fail; item += step, i++) {
+        tile_at<NT>(a, s_pre, item, &e, &t);
         const int b = i % TM::kBufs;
         // the accumulator's previous tile has been read out
         if (i >= TM::kBufs && !mbar_wait(&acc_empty[b], ((i / TM::kBufs) - 1) & 1)) {
@@ -333,31 +345,29 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         // columns on.  A scale address must be even, so 32-token tiles are
         // only used where a group has a single one (mx_plan).
         const uint32_t shift = NT == 64 ? (uint32_t)(t.local % 128) / 32 : 0u;
-        const int n_mma = (t.count + 15) & ~15;
+        const uint32_t idesc = mx_idesc<FMT>((t.count + 15) & ~15);
         bool ok = true;
         for (int st = st_lo; st < st_hi; st++, it++) {
           const int s = it % S::kStages;
-          if (!mbar_wait(&full[s], (it / S::kStages) & 1)) { ok = false; break; }
+          if (!mbar_wait(&scale_full[it & 1], (it >> 1) & 1) ||
+              !mbar_wait(&full[s], (it / S::kStages) & 1)) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
-          const int na = min(S::kAtoms, a.tiles_k - st * S::kAtoms);
-          for (int k = 0; k < na; k++) {
-            scale_copy(tmem + TM::kScaleW + 4 * k,
-                       scale_desc(smem_u32(sSW + s * S::kScale + k * kMxTileBytes)));
-#pragma unroll
-            for (int j = 0; j < S::kSub; j++)
-              scale_copy(tmem + TM::kScaleX + 4 * (k * S::kSub + j),
-                         scale_desc(smem_u32(sSX + (s * S::kSub + j) * S::kScale + k * kMxTileBytes)));
-          }
-          const uint32_t w0 = smem_u32(sW + s * kWTile), x0 = smem_u32(sX + s * S::kXTile);
+          const uint32_t sc = tmem + TM::kScale + (it & 1) * (TM::kScaleX + 16);
+          const uint32_t w0 = w_lo + s * (kWTile >> 4), x0 = x_lo + s * (S::kXTile >> 4);
           const int steps = min(kSteps, steps_all - st * kSteps);
-          for (int k = 0; k < steps; k++) {
-            const int atom = FMT == kMxE8m0 ? k / 2 : k;
-            const int id = FMT == kMxE8m0 ? (k & 1) * 2 : 0;
-            mma_mx<FMT>(d, sw128_desc(w0 + 32 * k), sw128_desc(x0 + 32 * k),
-                        mx_idesc<FMT>(n_mma, id), tmem + TM::kScaleW + 4 * atom,
-                        tmem + TM::kScaleX + 4 * S::kSub * atom + shift,
-                        (st > st_lo || k > 0) ? 1u : 0u);
-          }
+#pragma unroll
+          for (int k = 0; k < kSteps; k++)
+            if (k < steps) {
+              const int atom = FMT == kMxE8m0 ? k / 2 : k;
+              const int id = FMT == kMxE8m0 ? (k & 1) * 2 : 0;
+              mma_mx<FMT>(d, code_desc(w0 + 2 * k), code_desc(x0 + 2 * k),
+                          idesc | ((uint32_t)id << 4) | ((uint32_t)id << 29),
+                          sc + TM::kScaleX + 4 * atom, sc + 4 * S::kSub * atom + shift,
+                          (st > st_lo || k > 0) ? 1u : 0u);
+            }
           mma_commit(&empty[s]);
         }
         if (!ok) { s_fail = 1; break; }
@@ -365,56 +375,167 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         if (SPLIT) break;
       }
     }
+  } else if (warp < kEpiWarp) {
+    // scale tiles -> tensor memory: lane l's 16 bytes of a tile are the words
+    // of its rows l, l + 32, l + 64, l + 96, four consecutive columns
+    const uint32_t quadrant = (uint32_t)((warp & 3) * 32) << 16;
+    int it = 0;
+    bool ok = true;
+    for (int item = item0; item < items && ok; item += step) {
+      for (int st = st_lo; st < st_hi; st++, it++) {
+        const int s = it % S::kStages;
+        // the tile has landed, and the MMAs that read these columns (two
+        // stages ago) are complete
+        ok = mbar_wait(&full[s], (it / S::kStages) & 1);
+        if (ok && it >= 2)
+          ok = mbar_wait(&empty[(it - 2) % S::kStages], ((it - 2) / S::kStages) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          s_fail = 1;
+          break;
+        }
+        tc_fence_after();
+        uint32_t rw[4 * S::kAtoms], rx[4 * S::kAtoms * S::kSub];
+        const uint4* w = reinterpret_cast<const uint4*>(sSW + s * S::kScale) + lane;
+        const uint4* x = reinterpret_cast<const uint4*>(sSX + s * S::kSub * S::kScale) + lane;
+#pragma unroll
+        for (int k = 0; k < S::kAtoms; k++) {
+          const uint4 v = w[32 * k];
+          rw[4 * k] = v.x; rw[4 * k + 1] = v.y; rw[4 * k + 2] = v.z; rw[4 * k + 3] = v.w;
+#pragma unroll
+          for (int j = 0; j < S::kSub; j++) {
+            const uint4 u = x[32 * (j * S::kAtoms + k)];
+            uint32_t* o = rx + 4 * (k * S::kSub + j);
+            o[0] = u.x; o[1] = u.y; o[2] = u.z; o[3] = u.w;
+          }
+        }
+        const uint32_t sc = tmem + TM::kScale + (it & 1) * (TM::kScaleX + 16) + quadrant;
+        tmem_st<4 * S::kAtoms * S::kSub>(sc, rx);
+        tmem_st<4 * S::kAtoms>(sc + TM::kScaleX, rw);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&scale_full[it & 1]);
+      }
+      if (SPLIT) break;
+    }
   } else {
     wait_for_x();  // the row scales
-    const int q = warp & 3;             // the TMEM lane quadrant this warp may read
-    const int half = (warp - 2) >> 2;   // which half of the token columns
-    constexpr int NC = NT / 2;
+    const int q = warp & 3;                      // the TMEM lane quadrant this warp may read
+    const int part = (warp - kEpiWarp) >> 2;     // its share of the token columns
+    constexpr int NC = NT / (S::kEpiWarps / 4);
+    constexpr int CH = NC < 32 ? NC : 32;        // columns a thread takes at a time
+    static_assert(NC == CH || NC == 2 * CH, "columns");
+    float* gx = s_gx[warp - kEpiWarp];           // the row scales of its tokens
     TileAt t;
     int e = 0, i = 0;
-    for (int item = item0; tile_at<NT>(a, s_pre, item, &e, &t); item += step, i++) {
+    for (int item = item0; item < items; item += step, i++) {
+      tile_at<NT>(a, s_pre, item, &e, &t);
       const int b = i % TM::kBufs;
+      const int n = t.n0 + q * 32 + lane;
+      const bool nok = n < a.N;
+      const int mine = t.count - part * NC;  // this warp's tokens
+      float gw = 1.0f;
+      if (FMT == kMxE4m3 && !SPLIT) {  // fetched while the MMAs run
+        if (nok) gw = __ldg(a.gw + (int64_t)t.e * a.N + n);
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < NC; c += 32)
+          if (c + lane < NC)
+            gx[c + lane] = c + lane < mine ? __ldg(a.gx + t.row + part * NC + c + lane) : 0.0f;
+        __syncwarp();
+      }
       const bool got = __all_sync(0xffffffffu, mbar_wait(&acc_full[b], (i / TM::kBufs) & 1));
       tc_fence_after();
       const bool fail = !got || s_fail;
-      uint32_t r[NC];
-      if (!fail) {
-#pragma unroll
-        for (int c = 0; c < NC; c += 16)
-          if (half * NC + c < t.count)  // warp-uniform
-            tmem_ld16_nowait(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NT + half * NC + c),
-                             r + c);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (!SPLIT && lane == 0) mbar_arrive(&acc_empty[b]);
-      }
+      const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NT + part * NC);
       if (SPLIT) {
         // every MMA of this CTA is complete, so the stages are free
-        float* P = reinterpret_cast<float*>(base);
+        float* P = reinterpret_cast<float*>(base) + part * NC * kWRows + q * 32 + lane;
+#pragma unroll 1
+        for (int c0 = 0; c0 < NC && c0 < mine; c0 += 16) {
+          uint32_t r[16];
+          if (!fail) tmem_ld16_nowait(src + c0, r);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < NC; c++)
-          if (half * NC + c < t.count)
-            P[(half * NC + c) * kWRows + q * 32 + lane] =
-                fail ? __int_as_float(0x7fc00000) : __uint_as_float(r[c]);
+          for (int c = 0; c < 16; c++)
+            if (c0 + c < mine)
+              P[(c0 + c) * kWRows] = fail ? __int_as_float(0x7fc00000) : __uint_as_float(r[c]);
+        }
         break;
       }
-      const int n = t.n0 + q * 32 + lane;
-      const bool nok = n < a.N;
-      const float gw = FMT == kMxE4m3 && nok ? __ldg(a.gw + (int64_t)t.e * a.N + n) : 1.0f;
-      const int r0 = t.row + half * NC;
-      const int64_t y0 = (int64_t)r0 * a.ldy + n;
+      const int size_y = a.bf16_out ? 2 : 4;
+      const int64_t step_y = a.ldy * size_y;
+      char* y = static_cast<char*>(a.Y) + (int64_t)(t.row + part * NC) * step_y + (int64_t)n * size_y;
+      if (fail) {
+        for (int c = 0; c < min(mine, NC) && nok; c++, y += step_y) {
+          if (a.bf16_out) *reinterpret_cast<__nv_bfloat16*>(y) = __float2bfloat16_rn(__int_as_float(0x7fc00000));
+          else *reinterpret_cast<float*>(y) = __int_as_float(0x7fc00000);
+        }
+        break;  // the MMA warp stopped; nothing more to read
+      }
+      auto take = [&](int c0, uint32_t (&r)[CH]) {
 #pragma unroll
-      for (int c = 0; c < NC; c++) {
-        if (half * NC + c >= t.count) continue;  // warp-uniform
-        float v = fail ? __int_as_float(0x7fc00000) : __uint_as_float(r[c]);
-        if (FMT == kMxE4m3) v = __fmul_rn(__fmul_rn(v, __ldg(a.gx + r0 + c)), gw);
-        if (nok) {
-          if (a.bf16_out) static_cast<__nv_bfloat16*>(a.Y)[y0 + c * a.ldy] = __float2bfloat16_rn(v);
-          else static_cast<float*>(a.Y)[y0 + c * a.ldy] = v;
+        for (int c = 0; c < CH; c += 16) tmem_ld16_nowait(src + c0 + c, r + c);
+        tmem_wait_ld();
+        if (c0 + CH == NC) {  // the accumulator's last columns are in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[b]);
+        }
+        if (FMT == kMxE4m3) {
+#pragma unroll
+          for (int c = 0; c < CH; c += 4) {
+            const float4 g = *reinterpret_cast<const float4*>(gx + c0 + c);
+            const float gs[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+              r[c + j] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(r[c + j]), gs[j]), gw));
+          }
+        }
+      };
+      auto put_f32 = [&](int c0, const uint32_t (&r)[CH]) {
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+          if (nok && c0 + c < mine) *reinterpret_cast<uint32_t*>(y) = r[c];
+          y += step_y;
+        }
+      };
+      auto pack = [&](const uint32_t (&r)[CH], uint32_t (&h)[CH / 2]) {  // two tokens a register
+#pragma unroll
+        for (int c = 0; c < CH / 2; c++) {
+          const __nv_bfloat162 v =
+              __floats2bfloat162_rn(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
+          h[c] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+      };
+      auto put_bf16 = [&](int c0, const uint32_t (&h)[CH / 2]) {
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+          if (nok && c0 + c < mine)
+            *reinterpret_cast<uint16_t*>(y) = (uint16_t)(c & 1 ? h[c / 2] >> 16 : h[c / 2]);
+          y += step_y;
+        }
+      };
+      // The first columns are held as bf16 until the last ones have left
+      // tensor memory: the next tile's MMAs wait for loads, not for stores.
+      uint32_t r[CH], h[CH / 2];
+      take(0, r);
+      if (a.bf16_out) {
+        pack(r, h);
+        if (NC > CH) {
+          take(NC - CH, r);
+          put_bf16(0, h);
+          pack(r, h);
+        }
+        put_bf16(NC - CH, h);
+      } else {
+        put_f32(0, r);
+        if (NC > CH) {
+          take(NC - CH, r);
+          put_f32(NC - CH, r);
         }
       }
-      if (fail) break;  // the MMA warp stopped; nothing more to read
     }
   }
   tc_fence_before();
@@ -427,13 +548,14 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   if (SPLIT) {
     TileAt t;
     int e = 0;
-    const bool have = tile_at<NT>(a, s_pre, item0, &e, &t);  // the same for the whole cluster
+    const bool have = item0 < items;  // the same for the whole cluster
+    if (have) tile_at<NT>(a, s_pre, item0, &e, &t);
     cluster_sync_all();  // every CTA's partial is in its shared memory
     if (have) {
       const float* P = reinterpret_cast<const float*>(base);
       const int E = t.count * kWRows;
       const int e0 = (int)((int64_t)crank * E / csize), e1 = (int)((int64_t)(crank + 1) * E / csize);
-      for (int i = e0 + threadIdx.x; i < e1; i += kMxThreads) {
+      for (int i = e0 + threadIdx.x; i < e1; i += S::kThreads) {
         const int c = i / kWRows, n = t.n0 + i % kWRows;
         if (n < a.N) {
           float v = 0.0f;
@@ -453,21 +575,44 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-cudaError_t code_map(EncodeTiledFn enc, CUtensorMap* map, const uint8_t* codes, int64_t rows,
-                     int64_t K, int box_rows) {
-  const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
-  const cuuint32_t box[2] = {(cuuint32_t)kRowBytes, (cuuint32_t)box_rows};
+cudaError_t byte_map(EncodeTiledFn enc, CUtensorMap* map, const uint8_t* p, int64_t row_bytes,
+                     int64_t rows, int unit, int box_units, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)(row_bytes / unit), (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  const cuuint32_t box[2] = {(cuuint32_t)box_units, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims,
-                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r =
+      enc(map, unit == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT64, 2,
+          const_cast<uint8_t*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          unit == 1 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+struct Maps {
+  CUtensorMap x, w, sx, sw;
+};
+
+// Codes as bytes, 128 of a row at a time.  Scale tiles as 8-byte units, a
+// stage's tiles along K at a time (tiles past K read as zero) and as many
+// bands as a token tile has.
+cudaError_t make_maps(const MxTensor& x, const MxTensor& w, const MxPlan& p, int box, Maps* m) {
+  EncodeTiledFn enc = nullptr;
+  cudaError_t e = encode_fn(&enc);
+  const int64_t scale_row = mx_tiles_k(x.fmt, x.K) * kMxTileBytes;
+  const int units = (x.fmt == kMxE8m0 ? 2 : 4) * kMxTileBytes / 8;
+  if (e == cudaSuccess) e = byte_map(enc, &m->x, x.codes, x.K / 2, x.rows, 1, kRowBytes, box);
+  if (e == cudaSuccess) e = byte_map(enc, &m->w, w.codes, w.K / 2, w.rows, 1, kRowBytes, kWRows);
+  if (e == cudaSuccess)
+    e = byte_map(enc, &m->sx, x.scales, scale_row, mx_bands(x.rows, x.groups), 8, units,
+                 (p.nt + 127) / 128);
+  if (e == cudaSuccess)
+    e = byte_map(enc, &m->sw, w.scales, scale_row, mx_bands(w.rows, w.groups), 8, units, 1);
+  return e;
+}
+
 template <int FMT, int NT, bool SPLIT>
-cudaError_t launch_t(const CUtensorMap& xmap, const CUtensorMap& wmap, const MxGemmArgs& a,
+cudaError_t launch_t(const Maps& m, const MxGemmArgs& a,
                      const MxPlan& p, bool overlap, cudaStream_t st) {
   constexpr int smem = Shape<FMT, NT>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<FMT, NT, SPLIT>,
@@ -475,7 +620,7 @@ cudaError_t launch_t(const CUtensorMap& xmap, const CUtensorMap& wmap, const MxG
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = SPLIT ? dim3((unsigned)p.split, (unsigned)p.tiles, 1) : dim3((unsigned)p.ctas, 1, 1);
-  cfg.blockDim = dim3(kMxThreads, 1, 1);
+  cfg.blockDim = dim3(Shape<FMT, NT>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -494,25 +639,25 @@ cudaError_t launch_t(const CUtensorMap& xmap, const CUtensorMap& wmap, const MxG
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NT, SPLIT>, xmap, wmap, a);
+  return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NT, SPLIT>, m.x, m.w, m.sx, m.sw, a);
 }
 
 template <int FMT>
-cudaError_t launch_f(const CUtensorMap& xmap, const CUtensorMap& wmap, const MxGemmArgs& a,
+cudaError_t launch_f(const Maps& m, const MxGemmArgs& a,
                      const MxPlan& p, bool overlap, cudaStream_t st) {
   if (p.split > 1) {
     switch (p.nt) {
-      case 32: return launch_t<FMT, 32, true>(xmap, wmap, a, p, overlap, st);
-      case 64: return launch_t<FMT, 64, true>(xmap, wmap, a, p, overlap, st);
-      case 128: return launch_t<FMT, 128, true>(xmap, wmap, a, p, overlap, st);
-      default: return launch_t<FMT, 256, true>(xmap, wmap, a, p, overlap, st);
+      case 32: return launch_t<FMT, 32, true>(m, a, p, overlap, st);
+      case 64: return launch_t<FMT, 64, true>(m, a, p, overlap, st);
+      case 128: return launch_t<FMT, 128, true>(m, a, p, overlap, st);
+      default: return launch_t<FMT, 256, true>(m, a, p, overlap, st);
     }
   }
   switch (p.nt) {
-    case 32: return launch_t<FMT, 32, false>(xmap, wmap, a, p, overlap, st);
-    case 64: return launch_t<FMT, 64, false>(xmap, wmap, a, p, overlap, st);
-    case 128: return launch_t<FMT, 128, false>(xmap, wmap, a, p, overlap, st);
-    default: return launch_t<FMT, 256, false>(xmap, wmap, a, p, overlap, st);
+    case 32: return launch_t<FMT, 32, false>(m, a, p, overlap, st);
+    case 64: return launch_t<FMT, 64, false>(m, a, p, overlap, st);
+    case 128: return launch_t<FMT, 128, false>(m, a, p, overlap, st);
+    default: return launch_t<FMT, 256, false>(m, a, p, overlap, st);
   }
 }
 
@@ -538,21 +683,19 @@ MxPlan mx_plan(int groups, int64_t rows, int64_t N, int64_t K) {
 
 cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f32, int64_t ldy,
                            bool overlap, cudaStream_t st) {
-  EncodeTiledFn enc;
-  cudaError_t e = encode_fn(&enc);
-  if (e != cudaSuccess) return e;
   const int64_t N = w.rows / w.groups;
   const MxPlan p = mx_plan(x.groups, x.rows, N, x.K);
-  CUtensorMap xmap, wmap;
-  e = code_map(enc, &xmap, x.codes, x.rows, x.K, p.nt < 128 ? 32 : 64);
-  if (e == cudaSuccess) e = code_map(enc, &wmap, w.codes, w.rows, w.K, kWRows);
+  // One copy for all of a tile's token rows; ragged groups leave many tiles
+  // part empty and take pieces, of which only those with rows are fetched.
+  const int box = x.groups == 1 ? p.nt : (p.nt < 128 ? 32 : 64);
+  Maps m;
+  const cudaError_t e = make_maps(x, w, p, box, &m);
   if (e != cudaSuccess) return e;
-  const MxGemmArgs a{x.scales, w.scales, x.row_scale, w.row_scale, Y, ldy,
+  const MxGemmArgs a{x.row_scale, w.row_scale, Y, ldy,
                      MxRows{x.offsets, x.groups, (int)x.rows}, (int)N, (int)x.K,
-                     (int)((N + kWRows - 1) / kWRows), p.stages, (int)mx_tiles_k(x.fmt, x.K),
-                     f32 ? 0 : 1};
-  return x.fmt == kMxE8m0 ? launch_f<kMxE8m0>(xmap, wmap, a, p, overlap, st)
-                          : launch_f<kMxE4m3>(xmap, wmap, a, p, overlap, st);
+                     (int)((N + kWRows - 1) / kWRows), p.stages, box, f32 ? 0 : 1};
+  return x.fmt == kMxE8m0 ? launch_f<kMxE8m0>(m, a, p, overlap, st)
+                          : launch_f<kMxE4m3>(m, a, p, overlap, st);
 }
 
 cudaError_t mx_timeout_flag(unsigned int* out) {
