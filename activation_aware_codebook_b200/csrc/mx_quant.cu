@@ -26,6 +26,23 @@ namespace aaac {
 
 namespace {
 
+// Division of n < 2^31 by a fixed d: (n m) >> (31 + l) with l = ceil(log2 d)
+// and m = floor(2^(31 + l) / d) + 1; m d exceeds 2^(31 + l) by at most d <= 2^l,
+// so n times that excess stays below 2^(31 + l).
+struct Div {
+  uint32_t m, shift, d;
+  explicit Div(uint32_t d_) : d(d_) {
+    uint32_t l = 0;
+    while (((uint64_t)1 << l) < d) l++;
+    shift = 31 + l;
+    m = (uint32_t)(((uint64_t)1 << shift) / d + 1);
+    if (d == 1) m = 1, shift = 0;
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return (uint32_t)(((uint64_t)n * m) >> shift);
+  }
+};
+
 struct QuantArgs {
   const void* X;
   const int32_t* index;  // source row of each row, or NULL
@@ -36,12 +53,12 @@ struct QuantArgs {
   uint8_t* scales;
   float* row_scale;
   int64_t tiles_k;
+  Div per;  // rows of a group, where all groups are equal
 };
 
-// The group of row r (the number of later groups that start at or before it),
-// by the whole warp; -1 when r lies in no group.
+// The ragged group of row r (the number of later groups that start at or
+// before it), by the whole warp; -1 when r lies in no group.
 __device__ __forceinline__ int group_of(const MxRows& g, int r, int lane) {
-  if (!g.offsets) return min(r / (g.rows / g.groups), g.groups - 1);
   int e = 0;
   for (int i = 1; i <= g.groups; i += 32) {
     const bool before = i + lane <= g.groups && __ldg(g.offsets + min(i + lane, g.groups)) <= r;
@@ -52,19 +69,50 @@ __device__ __forceinline__ int group_of(const MxRows& g, int r, int lane) {
   return e >= g.groups || r < __ldg(g.offsets) ? -1 : e;
 }
 
-// Where row r of group e keeps its scale bytes (of the first tile along K).
-__device__ __forceinline__ int64_t scale_at(const MxRows& g, int e, int r, int64_t tiles_k) {
+// Where row r of group e, whose first row is `first`, keeps its scale bytes (of
+// the first tile along K).
+__device__ __forceinline__ int64_t scale_place(uint32_t e, uint32_t first, uint32_t r,
+                                               int64_t tiles_k) {
+  const uint32_t local = r - first, i = local % kMxTileRows;
+  return (int64_t)(first / kMxTileRows + e + local / kMxTileRows) * tiles_k * kMxTileBytes +
+         (i % 32) * 16 + i / 32 * 4;
+}
+__device__ __forceinline__ int64_t scale_equal(const Div& per, uint32_t r, int64_t tiles_k) {
+  const uint32_t e = per(r);
+  return scale_place(e, e * per.d, r, tiles_k);
+}
+// -1 for a row of no group; inside the tensor whatever the offsets say.
+__device__ __forceinline__ int64_t scale_ragged(const MxRows& g, int r, int lane,
+                                                int64_t tiles_k) {
+  const int e = group_of(g, r, lane);
+  if (e < 0) return -1;
   int first, last;
   mx_group(g, e, &first, &last);
-  const int local = max(r - first, 0);
-  const int64_t band = min((int64_t)first / kMxTileRows + e + local / kMxTileRows,
-                           mx_bands(g.rows, g.groups) - 1);
-  const int i = local % kMxTileRows;
-  return band * tiles_k * kMxTileBytes + (i % 32) * 16 + (i / 32) * 4;
+  return scale_place((uint32_t)e, (uint32_t)min(first, r), (uint32_t)r, tiles_k);
 }
 
+__device__ __forceinline__ float rcp_approx(float d) {  // within a step of 1 / d
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return r;
+}
+
+// x / d from r, a reciprocal of d: the quotient x r is off by steps, its
+// residual is exact in an fma, and adding the residual's quotient rounds to
+// the nearest (Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990; always so with r rounded to nearest, and
+// all but about one time in a million with r a step off).  Three instructions
+// where a division per value takes about ten.
+__device__ __forceinline__ float div_by(float x, float d, float r) {
+  const float q = __fmul_rn(x, r);
+  return __fmaf_rn(-r, __fmaf_rn(d, q, -x), q);  // these signs keep a zero's
+}
+
+// silu(a) b, each step in fp32.  exp(-a) is held below 2^126, so that its
+// reciprocal is a normal number: silu(a) is below 1e-35 there.
 __device__ __forceinline__ float silu_mul(float a, float b) {
-  return __fmul_rn(__fdiv_rn(a, __fadd_rn(1.0f, expf(-a))), b);
+  const float d = __fadd_rn(1.0f, expf(fminf(-a, 87.0f)));
+  return __fmul_rn(div_by(a, d, rcp_approx(d)), b);
 }
 
 // 16 values of a row.  bf16 stays packed: half the registers.
@@ -114,10 +162,18 @@ struct Run {
   __device__ __forceinline__ uint32_t amax() const {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; i++) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 0; i < 16; i++) {
+      float t;
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(t) : "f"(__uint_as_float(m)), "f"(fabsf(v[i])));
+      m = __float_as_uint(t);
+    }
     return m;
   }
-  __device__ __forceinline__ float get(int i) const { return v[i]; }
+  // half h's values times a power of two
+  __device__ __forceinline__ void scaled(int h, float f, float (&o)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; i++) o[i] = __fmul_rn(v[8 * h + i], f);
+  }
 };
 
 template <>
@@ -139,10 +195,29 @@ struct Run<false, false> {
     for (int i = 0; i < 8; i++) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
     return max(m << 16, m & 0xffff0000u);
   }
-  __device__ __forceinline__ float get(int i) const {
-    return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+  // The product is exact in bf16 too (below 2^-126, where it is not, the code
+  // is 0 either way): one multiply for two values.
+  __device__ __forceinline__ void scaled(int h, float f, float (&o)[8]) const {
+    const uint32_t f2 = __float_as_uint(f) | __float_as_uint(f) >> 16;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      uint32_t p;
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p) : "r"(w[4 * h + i]), "r"(f2));
+      o[2 * i] = bf16_lo(p);
+      o[2 * i + 1] = bf16_hi(p);
+    }
   }
 };
+
+// An E4M3 byte without its sign (a scale), exact in fp32.
+__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+  float f;
+  asm("{\n .reg .b16 b, l, h;\n .reg .b32 p;\n cvt.u16.u32 b, %1;\n"
+      " cvt.rn.f16x2.e4m3x2 p, b;\n mov.b32 {l, h}, p;\n cvt.f32.f16 %0, l;\n}\n"
+      : "=f"(f)
+      : "r"(byte & 0x7fu));
+  return f;
+}
 
 // Eight E2M1 codes of eight floats, the first in the lowest nibble; round to
 // nearest even, magnitudes above 6 to 6.
@@ -163,56 +238,55 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 
 // Codes and scale of one run, written out.  Every lane of the warp takes part
 // (the lanes of a scale word meet in shuffles); `in` says whether this lane's
-// run lies inside the row.  pbits: E4M3 only, the bits of 2^-p.
+// run lies inside the row.  down: E4M3 only, 2^-p.
 template <int FMT, bool F32, bool SWIGLU>
 __device__ __forceinline__ void emit(const Run<F32, SWIGLU>& run, bool in, int col, int lane,
                                      float down, bool bad_row, uint8_t* crow, uint8_t* srow) {
   const uint32_t own = run.amax();
-  uint32_t word;
-  uint32_t c[2];
+  uint32_t word, c[2];
   if (FMT == kMxE8m0) {
     const uint32_t m = max(own, __shfl_xor_sync(0xffffffffu, own, 1));
     const bool bad = m >= kInfBits;
     const uint32_t byte = bad ? 255u : (uint32_t)max((int)(m >> 23) - 2, 0);
     // byte <= 252 for finite values, so 2^(127 - byte) is a normal number
-    const float inv = bad ? 0.0f : __uint_as_float((254u - byte) << 23);
+    const float inv = __uint_as_float((254u - byte) << 23);
 #pragma unroll
     for (int h = 0; h < 2; h++) {
       float q[8];
-#pragma unroll
-      for (int i = 0; i < 8; i++) q[i] = bad ? 0.0f : __fmul_rn(run.get(8 * h + i), inv);
-      c[h] = e2m1x8(q);
+      run.scaled(h, inv, q);
+      c[h] = bad ? 0u : e2m1x8(q);
     }
     word = in ? byte << (8 * ((lane >> 1) & 3)) : 0u;
     word |= __shfl_xor_sync(0xffffffffu, word, 2);
     word |= __shfl_xor_sync(0xffffffffu, word, 4);
   } else {
-    const float top = bad_row ? 0.0f : __fmul_rn(__uint_as_float(own), down);
-    const uint32_t byte =
-        (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(top, 6.0f), __NV_SATFINITE, __NV_E4M3);
-    const float s = e4m3_mag(byte);
-    const bool none = byte == 0u || bad_row;
-    // The quotient x' / s, x' = x * 2^-p.  For bf16 inputs: with r = 1/s
-    // rounded towards zero and rl = fp32_RN(1/s - r) >= 0, fma(x', r, x' * rl)
-    // is the quotient to within 2^-24 (1 + 2^-21) of it, and exactly the
-    // quotient where that is a number of few bits (and keeps the sign of a
-    // zero).  A border between codes is such a number, and a quotient of an
-    // 8-bit x' and a 4-bit s that is not on a border is 2^-9 or more away
-    // from it; so every code is the one that the exact quotient has, without
-    // a division per value.  fp32 inputs have no such gap and take the
-    // correctly rounded division.
-    const float r = none ? 0.0f : __frcp_rz(s);
-    const float rl = none ? 0.0f : __fmul_rn(__fmaf_rn(-s, r, 1.0f), r);
+    const float top = __fmul_rn(__uint_as_float(own), down);
+    const uint32_t byte = bad_row ? 0u
+                                  : (uint32_t)__nv_cvt_float_to_fp8(
+                                        div_by(top, 6.0f, 1.0f / 6.0f), __NV_SATFINITE, __NV_E4M3);
+    const float s = e4m3_value(byte);
+    // The quotient x' / s, x' = x * 2^-p.
+    // bf16: with r a little below 1/s and rl = fp32_RN(r (1 - s r)) > 0, the
+    // rest of 1/s, fma(x', r, x' rl) is the quotient to within 2^-24 (1 +
+    // 2^-19) of it, and exactly the quotient where that is a number of few
+    // bits (and keeps a zero's sign).  A border between codes is such a
+    // number, and a quotient of an 8-bit x' and a 4-bit s that is not on a
+    // border is 2^-9 or more away from it; so every code is the one that the
+    // exact quotient has.
+    // fp32 values have no such gap and take the correctly rounded quotient
+    // (its residual can only underflow where the code is 0 anyway).
+    float r = rcp_approx(s);
+    if (F32 || SWIGLU) r = __fmaf_rn(__fmaf_rn(-s, r, 1.0f), r, r);
+    else r = __fmul_rn(r, 1.0f - 0x1p-22f);
+    const float rl = __fmul_rn(__fmaf_rn(-s, r, 1.0f), r);
 #pragma unroll
     for (int h = 0; h < 2; h++) {
       float q[8];
+      run.scaled(h, down, q);
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const float x = none ? 0.0f : __fmul_rn(run.get(8 * h + i), down);
-        q[i] = (F32 || SWIGLU) ? (none ? 0.0f : __fdiv_rn(x, s))
-                               : __fmaf_rn(x, r, __fmul_rn(x, rl));
-      }
-      c[h] = e2m1x8(q);
+      for (int i = 0; i < 8; i++)
+        q[i] = (F32 || SWIGLU) ? div_by(q[i], s, r) : __fmaf_rn(q[i], r, __fmul_rn(q[i], rl));
+      c[h] = byte == 0u ? 0u : e2m1x8(q);
     }
     word = in ? byte << (8 * (lane & 3)) : 0u;
     word |= __shfl_xor_sync(0xffffffffu, word, 1);
@@ -250,8 +324,9 @@ quantize_kernel(const __grid_constant__ QuantArgs a) {
       else run[c].zero();
     }
   }
-  const int e = group_of(a.rows, row, lane);
-  if (e < 0) return;  // the whole block: a row of no group stays as it was
+  const int64_t at = a.rows.offsets ? scale_ragged(a.rows, row, lane, a.tiles_k)
+                                    : scale_equal(a.per, (uint32_t)row, a.tiles_k);
+  if (at < 0) return;  // the whole block: a row of no group stays as it was
   float down = 1.0f;
   bool bad_row = false;
   if (FMT == kMxE4m3) {
@@ -279,7 +354,7 @@ quantize_kernel(const __grid_constant__ QuantArgs a) {
       a.row_scale[row] = __uint_as_float(bad_row ? 0x7fc00000u : (uint32_t)(127 + p) << 23);
   }
   uint8_t* crow = a.codes + (int64_t)row * (a.K >> 1);
-  uint8_t* srow = a.scales + scale_at(a.rows, e, row, a.tiles_k);
+  uint8_t* srow = a.scales + at;
   if (C) {
 #pragma unroll
     for (int c = 0; c < kHeld; c++) {
@@ -297,76 +372,172 @@ quantize_kernel(const __grid_constant__ QuantArgs a) {
   }
 }
 
+// Runs a thread holds.  With many rows: enough that a block's loads cover the
+// time its predecessor on the SM takes to compute and leave (8192 x 14336 to
+// E8M0: 78 us at one run a thread).  With few rows: one, for the most threads.
 template <int FMT, bool F32, bool SWIGLU>
 void launch_quantize_t(const QuantArgs& a, cudaStream_t st) {
+  constexpr int kMany = F32 || SWIGLU ? 2 : 4;
   const int runs = a.K >> 4;
   auto threads = [](int n) { return n < 1024 ? (n + 31) / 32 * 32 : 1024; };
   const unsigned grid = (unsigned)a.rows.rows;
-  if (runs <= 1024)
-    quantize_kernel<FMT, F32, SWIGLU, 1><<<grid, threads(runs), 0, st>>>(a);
-  else if (runs <= 2048)
-    quantize_kernel<FMT, F32, SWIGLU, 2><<<grid, threads((runs + 1) / 2), 0, st>>>(a);
-  else
+  if (runs > 1024 * kMany)
     quantize_kernel<FMT, F32, SWIGLU, 0><<<grid, 1024, 0, st>>>(a);
+  else if (runs > 1024 || (!SWIGLU && a.rows.rows >= 4 * 148))
+    quantize_kernel<FMT, F32, SWIGLU, kMany><<<grid, threads((runs + kMany - 1) / kMany), 0, st>>>(a);
+  else
+    quantize_kernel<FMT, F32, SWIGLU, 1><<<grid, threads(runs), 0, st>>>(a);
 }
 
-// Back to bf16 or fp32: E2M1 * scale * row scale, exact in fp32 (2 + 4 bits).
-// A block walks rows; consecutive lanes take consecutive 8-value pieces (4
-// bytes of codes in, 16 or 32 bytes out).
-template <int FMT, bool F32>
-__global__ void __launch_bounds__(256)
-mx_dequant_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                  const float* __restrict__ row_scale, MxRows rows, int K, int64_t tiles_k,
-                  void* __restrict__ out, int64_t ldo) {
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x;
-  const int e = group_of(rows, row, lane);
-  if (e < 0) return;
-  const uint32_t* crow = reinterpret_cast<const uint32_t*>(codes + (int64_t)row * (K >> 1));
-  const uint8_t* srow = scales + scale_at(rows, e, row, tiles_k);
-  const float g = FMT == kMxE4m3 ? __ldg(row_scale + row) : 1.0f;
-  constexpr int kPieces = FMT == kMxE8m0 ? 4 : 2;  // 8-value pieces of a block
-#pragma unroll 4
-  for (int i = threadIdx.x; i < (K >> 3); i += blockDim.x) {
-    const uint32_t w = __ldg(crow + i);
-    const int b = i / kPieces;
-    const uint32_t sb = __ldg(srow + (int64_t)(b >> 2) * kMxTileBytes + (b & 3));
-    float s;
-    if (FMT == kMxE8m0)  // 2^(byte - 127); 255 is NaN
-      s = sb == 255u ? __uint_as_float(0x7fc00000u)
-                     : __uint_as_float(sb ? sb << 23 : 0x00400000u);
-    else
-      s = __fmul_rn(e4m3_mag(sb & 0x7fu), g);
-    float v[8];
+// 16 values from two words of codes: E2M1 * s, exact in fp32.
+__device__ __forceinline__ void expand16(uint2 w, float s, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
     uint32_t h[4];
     asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
         " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
         " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
+        : "r"(i ? w.y : w.x));
 #pragma unroll
     for (int j = 0; j < 4; j++) {
       float lo, hi;
       asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}\n"
           : "=f"(lo), "=f"(hi)
           : "r"(h[j]));
-      v[2 * j] = __fmul_rn(lo, s);
-      v[2 * j + 1] = __fmul_rn(hi, s);
+      v[8 * i + 2 * j] = __fmul_rn(lo, s);
+      v[8 * i + 2 * j + 1] = __fmul_rn(hi, s);
     }
-    if (F32) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row * ldo + 8 * (int64_t)i);
-      o[0] = make_float4(v[0], v[1], v[2], v[3]);
-      o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint32_t p[4];
+  }
+}
+
+// The scale a byte stands for, times the row's g.
+template <int FMT>
+__device__ __forceinline__ float scale_value(uint32_t byte, float g) {
+  if (FMT == kMxE4m3) return __fmul_rn(e4m3_value(byte), g);
+  return byte == 255u ? __uint_as_float(0x7fc00000u)  // 2^(byte - 127); 255 is NaN
+                      : __uint_as_float(byte ? byte << 23 : 0x00400000u);
+}
+
+// 32 bytes of a row: one 32-byte store where rows are so aligned.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void store16(void* out, int64_t at, const float (&v)[16], bool wide) {
+  uint32_t w[8];
+  if (F32) {
+    float* o = static_cast<float*>(out) + at;
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        p[j] = *reinterpret_cast<const uint32_t*>(&t);
-      }
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row * ldo + 8 * (int64_t)i) =
-          make_uint4(p[0], p[1], p[2], p[3]);
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) w[i] = __float_as_uint(v[8 * h + i]);
+      store32(o + 8 * h, w, wide);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+    store32(static_cast<uint16_t*>(out) + at, w, wide);
+  }
+}
+
+struct DequantArgs {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* row_scale;
+  MxRows rows;
+  int K;
+  int64_t tiles_k;
+  void* out;
+  int64_t ldo;
+  bool wide;
+};
+
+template <int FMT>
+__device__ __forceinline__ int64_t scale_step(int run) {  // a run's byte within its row
+  const int b = FMT == kMxE8m0 ? run >> 1 : run;
+  return (int64_t)(b >> 2) * kMxTileBytes + (b & 3);
+}
+
+// Back to bf16 or fp32.  Groups of equal size: the tensor's 16-value runs, four
+// to a thread (its loads together), whatever the row length; 8 bytes of codes
+// and a scale byte in, one 32-byte store (two for fp32) out.
+constexpr int kDeqThreads = 256, kDeqRuns = 4;
+template <int FMT, bool F32>
+__global__ void __launch_bounds__(kDeqThreads)
+mx_dequant_kernel(const __grid_constant__ DequantArgs a, int row0, uint32_t total, Div runs,
+                  Div per) {
+  const uint32_t i0 = blockIdx.x * (kDeqThreads * kDeqRuns) + threadIdx.x;
+  uint2 w[kDeqRuns];
+  uint32_t sb[kDeqRuns];
+  float g[kDeqRuns];
+  int row[kDeqRuns], run[kDeqRuns];
+#pragma unroll
+  for (int u = 0; u < kDeqRuns; u++) {
+    const uint32_t i = min(i0 + u * kDeqThreads, total - 1);
+    const uint32_t r = runs(i);
+    row[u] = row0 + (int)r;
+    run[u] = (int)(i - r * runs.d);
+    const uint8_t* srow = a.scales + scale_equal(per, (uint32_t)row[u], a.tiles_k);
+    w[u] = __ldg(reinterpret_cast<const uint2*>(a.codes + (int64_t)row[u] * (a.K >> 1)) + run[u]);
+    sb[u] = __ldg(srow + scale_step<FMT>(run[u]));
+    g[u] = FMT == kMxE4m3 ? __ldg(a.row_scale + row[u]) : 1.0f;
+  }
+#pragma unroll
+  for (int u = 0; u < kDeqRuns; u++) {
+    float v[16];
+    expand16(w[u], scale_value<FMT>(sb[u], g[u]), v);
+    if (i0 + u * kDeqThreads < total)
+      store16<F32>(a.out, row[u] * a.ldo + 16 * (int64_t)run[u], v, a.wide);
+  }
+}
+
+// Ragged groups: a block a row, its group found once.
+template <int FMT, bool F32>
+__global__ void __launch_bounds__(kDeqThreads)
+mx_dequant_ragged_kernel(const __grid_constant__ DequantArgs a) {
+  const int row = blockIdx.x;
+  const int64_t at = scale_ragged(a.rows, row, threadIdx.x & 31, a.tiles_k);
+  if (at < 0) return;
+  const uint2* crow = reinterpret_cast<const uint2*>(a.codes + (int64_t)row * (a.K >> 1));
+  const uint8_t* srow = a.scales + at;
+  const float g = FMT == kMxE4m3 ? __ldg(a.row_scale + row) : 1.0f;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < (a.K >> 4); i += blockDim.x) {
+    float v[16];
+    expand16(__ldg(crow + i), scale_value<FMT>(__ldg(srow + scale_step<FMT>(i)), g), v);
+    store16<F32>(a.out, row * a.ldo + 16 * (int64_t)i, v, a.wide);
+  }
+}
+
+template <int FMT, bool F32>
+void launch_dequant_t(const DequantArgs& a, cudaStream_t st) {
+  const int runs = a.K >> 4;
+  if (a.rows.offsets) {
+    mx_dequant_ragged_kernel<FMT, F32><<<(unsigned)a.rows.rows,
+                                         runs < kDeqThreads ? (runs + 31) / 32 * 32 : kDeqThreads, 0,
+                                         st>>>(a);
+    return;
+  }
+  // as many rows to a launch as 2^30 runs hold
+  const int64_t step = ((int64_t)1 << 30) / runs;
+  for (int64_t r0 = 0; r0 < a.rows.rows; r0 += step) {
+    const int64_t n = a.rows.rows - r0 < step ? a.rows.rows - r0 : step;
+    const uint32_t total = (uint32_t)(n * runs);
+    const unsigned grid = (total + kDeqThreads * kDeqRuns - 1) / (kDeqThreads * kDeqRuns);
+    mx_dequant_kernel<FMT, F32><<<grid, kDeqThreads, 0, st>>>(
+        a, (int)r0, total, Div((uint32_t)runs), Div((uint32_t)(a.rows.rows / a.rows.groups)));
   }
 }
 
@@ -379,7 +550,7 @@ size_t mx_scale_bytes(int fmt, int64_t rows, int64_t K, int groups) {
 cudaError_t launch_mx_quantize(const MxSource& x, const MxTensor& q, cudaStream_t st) {
   QuantArgs a{x.X, x.index, x.ldx, (int)x.rows, (int)q.K,
               MxRows{q.offsets, q.groups, (int)q.rows}, q.codes, q.scales, q.row_scale,
-              mx_tiles_k(q.fmt, q.K)};
+              mx_tiles_k(q.fmt, q.K), Div((uint32_t)(q.rows / q.groups ? q.rows / q.groups : 1))};
   if (q.fmt == kMxE8m0) {
     if (x.f32) {
       if (x.swiglu) launch_quantize_t<kMxE8m0, true, true>(a, st);
@@ -402,18 +573,16 @@ cudaError_t launch_mx_quantize(const MxSource& x, const MxTensor& q, cudaStream_
 
 cudaError_t launch_mx_dequant(const MxTensor& q, void* out, bool f32, int64_t ldo,
                               cudaStream_t st) {
-  const MxRows rows{q.offsets, q.groups, (int)q.rows};
-  const int pieces = (int)(q.K >> 3);
-  const int threads = pieces < 256 ? (pieces + 31) / 32 * 32 : 256;
-  const unsigned grid = (unsigned)q.rows;
-  const int K = (int)q.K;
-  const int64_t tk = mx_tiles_k(q.fmt, q.K);
+  const int size = f32 ? 4 : 2;
+  const DequantArgs a{q.codes, q.scales, q.row_scale, MxRows{q.offsets, q.groups, (int)q.rows},
+                      (int)q.K, mx_tiles_k(q.fmt, q.K), out, ldo,
+                      reinterpret_cast<uintptr_t>(out) % 32 == 0 && ldo * size % 32 == 0};
   if (q.fmt == kMxE8m0) {
-    if (f32) mx_dequant_kernel<kMxE8m0, true><<<grid, threads, 0, st>>>(q.codes, q.scales, q.row_scale, rows, K, tk, out, ldo);
-    else mx_dequant_kernel<kMxE8m0, false><<<grid, threads, 0, st>>>(q.codes, q.scales, q.row_scale, rows, K, tk, out, ldo);
+    if (f32) launch_dequant_t<kMxE8m0, true>(a, st);
+    else launch_dequant_t<kMxE8m0, false>(a, st);
   } else {
-    if (f32) mx_dequant_kernel<kMxE4m3, true><<<grid, threads, 0, st>>>(q.codes, q.scales, q.row_scale, rows, K, tk, out, ldo);
-    else mx_dequant_kernel<kMxE4m3, false><<<grid, threads, 0, st>>>(q.codes, q.scales, q.row_scale, rows, K, tk, out, ldo);
+    if (f32) launch_dequant_t<kMxE4m3, true>(a, st);
+    else launch_dequant_t<kMxE4m3, false>(a, st);
   }
   return cudaGetLastError();
 }
