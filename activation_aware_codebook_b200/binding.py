@@ -535,9 +535,9 @@ def mx_workspace_size(fmt: int, rows: int, K: int, groups: int = 1) -> int:
 
 def mx_launch_plan(groups: int, rows: int, N: int, K: int) -> dict:
     """Host-only: the product's plan for these sizes (see aaac_mx_launch_plan)."""
-    out = (ctypes.c_int32 * 5)()
+    out = (ctypes.c_int32 * 6)()
     _check(load().aaac_mx_launch_plan(groups, rows, N, K, out))
-    return dict(zip(("columns", "split", "ctas", "stages", "tiles"), list(out)))
+    return dict(zip(("columns", "split", "ctas", "stages", "tiles", "rows"), list(out)))
 
 
 class MxTensor:

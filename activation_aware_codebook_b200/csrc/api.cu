@@ -816,6 +816,7 @@ aaac_status aaac_mx_launch_plan(int32_t groups, int64_t rows, int64_t N, int64_t
   out[2] = p.ctas;
   out[3] = p.stages;
   out[4] = (int32_t)p.tiles;
+  out[5] = p.pair ? 256 : 128;
   return ok();
 }
 

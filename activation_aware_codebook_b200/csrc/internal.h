@@ -157,6 +157,7 @@ struct MxTensor {
 struct MxPlan {
   int nt;         // token columns of a tile
   int split;      // CTAs that share a tile's K (1: persistent CTAs over the tiles)
+  int pair;       // 1: two CTAs to a tile of 256 weight rows
   int ctas;
   int stages;     // 256-column stages of K
   int64_t tiles;  // an upper bound for ragged groups

@@ -12,8 +12,7 @@
 //   warp 0      one lane issues four TMA copies: both code tiles
 //               (SWIZZLE_128B) and both operands' scale tiles;
 //   warps 2..5  bring the scale tiles from shared to tensor memory, one lane
-//               quadrant each (the tensor core wants a copy in all four), two
-//               stages in turn;
+//               quadrant each (the tensor core wants a copy in all four);
 //   warp 1      one lane issues four MMAs of K = 64;
 //   the others  epilogue: tensor memory -> registers, the accumulator handed
 //               back, row scales, stores.
@@ -51,34 +50,43 @@ struct MxGemmArgs {
   int64_t ldy;
   MxRows rows;        // of X and Y
   int N, K;
-  int n_tiles;        // 128-row weight tiles per group
+  int n_tiles;        // weight tiles per group
   int stages;         // ceil(K / 256)
   int box;            // token rows of one TMA copy
   int bf16_out;
 };
 
-template <int FMT, int NT>
+// How the CTAs of a launch share the work.
+constexpr int kWalk = 0;   // each walks tiles of 128 weight rows on its own
+constexpr int kSplit = 1;  // a cluster's CTAs each take a part of one tile's K
+constexpr int kPair = 2;   // two CTAs walk tiles of 256 weight rows (cta_group::2)
+
+template <int FMT, int NT, int MODE>
 struct Shape {
+  static constexpr bool kTwo = MODE == kPair;
+  static constexpr int kTileRows = kTwo ? 2 * kWRows : kWRows;  // weight rows of a tile
   static constexpr int kSub = (NT + 127) / 128;             // 128-row scale bands of a token tile
   static constexpr int kAtoms = FMT == kMxE8m0 ? 2 : 4;     // scale tiles of a stage along K
   static constexpr int kScale = kAtoms * kMxTileBytes;      // of one band
-  static constexpr int kXTile = NT * kRowBytes;
+  static constexpr int kXTile = (kTwo ? NT / 2 : NT) * kRowBytes;  // a pair's CTAs hold half each
   static constexpr int kStage = kWTile + kXTile + kScale * (1 + kSub);
   // 64 columns an epilogue thread at most: all of them leave tensor memory in
   // one go, so that the next tile's MMAs wait for no store
   static constexpr int kEpiWarps = NT == 256 ? 16 : 8;
   static constexpr int kThreads = (kEpiWarp + kEpiWarps) * 32;
-  static constexpr int kStages = NT == 256 ? 4 : (NT == 128 ? 6 : (NT == 64 ? 7 : 8));
-  static constexpr int kSmem = 1024 + kStages * kStage + (2 * kStages + 6) * 8 + 16;
+  static constexpr int kStages = kTwo ? 5 : (NT == 256 ? 4 : (NT == 128 ? 6 : (NT == 64 ? 7 : 8)));
+  static constexpr int kSmem = 1024 + kStages * kStage + (3 * kStages + 4) * 8 + 16;
   static_assert(kSmem + 4 * (kMxMaxGroups + 1) + 16 * NT + 64 <= kSmemLimit, "shared memory");
 };
 
-template <int NT, bool SPLIT>
+template <int NT, int MODE, int STAGES>
 struct Tmem {
-  static constexpr int kBufs = SPLIT || NT == 256 ? 1 : 2;  // accumulators
+  static constexpr int kBufs = MODE == kSplit || NT == 256 ? 1 : 2;  // accumulators
   static constexpr int kScale = kBufs * NT;                 // first scale column
   static constexpr int kScaleX = 16 * ((NT + 127) / 128);   // of a stage: X's columns, then 16 of W
-  static constexpr int kUsed = kScale + 2 * (kScaleX + 16); // two stages in turn
+  // as many sets as stages: a set is free when its stage is, with no wait of its own
+  static constexpr int kUsed = kScale + STAGES * (kScaleX + 16);
+  static_assert(kUsed <= 512, "tensor memory");
   static constexpr int kCols = kUsed <= 64 ? 64 : (kUsed <= 128 ? 128 : (kUsed <= 256 ? 256 : 512));
 };
 
@@ -92,28 +100,55 @@ __device__ __forceinline__ uint64_t code_desc(uint32_t at) {
 // UE4M3), M >> 7 at bit 27; the scale words' byte offsets of B at bit 4 and of
 // A at bit 29.
 template <int FMT>
-__device__ __forceinline__ uint32_t mx_idesc(int N) {
+__device__ __forceinline__ uint32_t mx_idesc(int M, int N) {
   return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
-         ((FMT == kMxE8m0 ? 1u : 0u) << 23) | (1u << 27);
+         ((FMT == kMxE8m0 ? 1u : 0u) << 23) | ((uint32_t)(M >> 7) << 27);
 }
 
-template <int FMT>
+#define AAAC_MX_MMA(GROUP, VEC)                                                          \
+  asm volatile(                                                                          \
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"                                      \
+      " tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC     \
+      " [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),                                 \
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)              \
+      : "memory")
+template <int FMT, bool TWO>
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t sa, uint32_t sb, uint32_t accumulate) {
-  if (FMT == kMxE8m0)
+  if (FMT == kMxE8m0) {
+    if (TWO) AAAC_MX_MMA("2", "2X");
+    else AAAC_MX_MMA("1", "2X");
+  } else {
+    if (TWO) AAAC_MX_MMA("2", "4X");
+    else AAAC_MX_MMA("1", "4X");
+  }
+}
+#undef AAAC_MX_MMA
+
+// The barrier (of both CTAs of a pair) completes with the MMAs issued so far.
+template <bool TWO>
+__device__ __forceinline__ void commit_mx(uint64_t* bar) {
+  if (TWO)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X"
-        " [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
         : "memory");
   else
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X"
-        " [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
+    mma_commit(bar);
+}
+
+// An arrival at the first CTA's barrier, from either CTA of a pair.
+template <bool TWO>
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  if (TWO) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at)
+                 : "memory");
+  } else {
+    mbar_arrive(bar);
+  }
 }
 
 // N consecutive columns of this warp's lane quadrant, from registers.
@@ -166,9 +201,40 @@ struct TileAt {
   int first;   // the group's first row
 };
 
+// True in one lane of the warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(p));
+  return p != 0;
+}
+// A wait of the whole warp, with one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+// A walk around the stages: the stage and the parity of its use.
+template <int STAGES>
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == STAGES) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// The tensor core's N for `count` tokens; a pair's CTAs hold half of it each.
+template <bool TWO>
+__device__ __forceinline__ int mma_n(int count) {
+  return TWO ? (count + 31) & ~31 : (count + 15) & ~15;
+}
+
 // Tile `item`, one of the s_pre[groups] * n_tiles; *e (the search's start) only
 // moves forward.
-template <int NT>
+template <int NT, int ROWS>
 __device__ __forceinline__ void tile_at(const MxGemmArgs& a, const int* s_pre, int item, int* e,
                                         TileAt* t) {
   while (item >= s_pre[*e + 1] * a.n_tiles) (*e)++;
@@ -177,19 +243,20 @@ __device__ __forceinline__ void tile_at(const MxGemmArgs& a, const int* s_pre, i
   int last;
   mx_group(a.rows, *e, &t->first, &last);
   t->e = *e;
-  t->n0 = (at / tt) * kWRows;
+  t->n0 = (at / tt) * ROWS;
   t->local = (at % tt) * NT;
   t->row = t->first + t->local;
   t->count = min(NT, last - t->row);
 }
 
-template <int FMT, int NT, bool SPLIT>
-__global__ void __launch_bounds__((Shape<FMT, NT>::kThreads), 1)
+template <int FMT, int NT, int MODE>
+__global__ void __launch_bounds__((Shape<FMT, NT, MODE>::kThreads), 1)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                const __grid_constant__ CUtensorMap sxmap, const __grid_constant__ CUtensorMap swmap,
                const __grid_constant__ MxGemmArgs a) {
-  using S = Shape<FMT, NT>;
-  using TM = Tmem<NT, SPLIT>;
+  using S = Shape<FMT, NT, MODE>;
+  using TM = Tmem<NT, MODE, S::kStages>;
+  constexpr bool SPLIT = MODE == kSplit, TWO = S::kTwo;
   extern __shared__ __align__(1024) unsigned char gsm[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(gsm) + 1023) & ~(uintptr_t)1023);
@@ -201,13 +268,17 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   uint64_t* empty = full + S::kStages;
   uint64_t* acc_full = empty + S::kStages;  // [2]
   uint64_t* acc_empty = acc_full + 2;       // [2]
-  uint64_t* scale_full = acc_empty + 2;     // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scale_full + 2);
+  uint64_t* scale_full = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scale_full + S::kStages);
   __shared__ int s_pre[kMxMaxGroups + 1];  // token tiles of the groups before
   __shared__ __align__(16) float s_gx[S::kEpiWarps][FMT == kMxE4m3 && !SPLIT ? NT / (S::kEpiWarps / 4) : 4];
   __shared__ int s_fail;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The same in every lane, and known to be: the roles of warps 0 and 1 run as
+  // whole warps, of which one lane issues, so that addresses and descriptors
+  // are worked out in uniform registers, where TMA and MMA want them.
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < a.rows.groups; e += S::kThreads) {
     int first, last;
     mx_group(a.rows, e, &first, &last);
@@ -217,21 +288,28 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     for (int s = 0; s < S::kStages; s++) {
       mbar_init(&full[s], 1);   // the producer's expect_tx
       mbar_init(&empty[s], 1);  // MMA commit
+      mbar_init(&scale_full[s], TWO ? 8 : 4);  // one arrive per scale warp
     }
     for (int b = 0; b < 2; b++) {
-      mbar_init(&acc_full[b], 1);              // MMA commit of a tile
-      mbar_init(&acc_empty[b], S::kEpiWarps);  // one arrive per epilogue warp
-      mbar_init(&scale_full[b], 4);            // one arrive per scale warp
+      mbar_init(&acc_full[b], 1);                              // MMA commit of a tile
+      mbar_init(&acc_empty[b], S::kEpiWarps * (TWO ? 2 : 1));  // one arrive per epilogue warp
     }
     s_fail = 0;
     s_pre[0] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(tmem_slot)),
-                 "r"(TM::kCols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if (TWO) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(tmem_slot)),
+                   "r"(TM::kCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(tmem_slot)),
+                   "r"(TM::kCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -253,12 +331,14 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
 
   // this CTA's tiles and its share of K
   uint32_t crank = 0, csize = 1;
-  if (SPLIT) {
+  if (MODE != kWalk) {
     crank = cluster_rank();
     csize = cluster_size();
   }
-  const int item0 = SPLIT ? blockIdx.y : blockIdx.x;
-  const int step = SPLIT ? 0 : gridDim.x;
+  if (TWO) cluster_sync_all();  // both CTAs' barriers are set up
+  const int item0 = SPLIT ? blockIdx.y : (TWO ? blockIdx.x / 2 : blockIdx.x);
+  const int step = SPLIT ? 0 : (TWO ? gridDim.x / 2 : gridDim.x);
+  const int wrow = TWO ? (int)crank * kWRows : 0;  // this CTA's first row of a tile
   const int st_lo = SPLIT ? (int)((int64_t)crank * a.stages / csize) : 0;
   const int st_hi = SPLIT ? (int)((int64_t)(crank + 1) * a.stages / csize) : a.stages;
 
@@ -266,130 +346,135 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   const int items = s_pre[a.rows.groups] * a.n_tiles;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // coordinates of a tile's copies: the rows of the codes and the bands of
-      // the scales, of both operands
-      struct At {
-        int w, sw, x, sx, boxes;
-      };
-      auto at_of = [&](const TileAt& t) {
-        At c;
-        c.w = t.e * a.N + t.n0;
-        c.sw = (int)((int64_t)t.e * a.N / kMxTileRows) + t.e + t.n0 / kMxTileRows;
-        c.x = t.row;
-        c.sx = t.first / kMxTileRows + t.e + t.local / kMxTileRows;
-        c.boxes = (t.count + a.box - 1) / a.box;  // only boxes that hold rows of the tile
-        return c;
-      };
-      const uint32_t box_bytes = (uint32_t)(a.box * kRowBytes);
-      auto load_w = [&](const At& c, int st, int s) {
+    const bool one = elect_one();
+    // coordinates of a tile's copies: the rows of the codes and the bands of
+    // the scales, of both operands
+    struct At {
+      int w, sw, x, sx, boxes;
+    };
+    auto at_of = [&](const TileAt& t) {
+      At c;
+      c.w = t.e * a.N + t.n0 + wrow;
+      c.sw = (int)((int64_t)t.e * a.N / kMxTileRows) + t.e + (t.n0 + wrow) / kMxTileRows;
+      const int half = mma_n<TWO>(t.count) / 2;
+      c.x = t.row + (TWO ? (int)crank * half : 0);
+      c.sx = t.first / kMxTileRows + t.e + t.local / kMxTileRows;
+      // only boxes that hold rows of the tile
+      c.boxes = ((TWO ? half : t.count) + a.box - 1) / a.box;
+      return c;
+    };
+    const uint32_t box_bytes = (uint32_t)(a.box * kRowBytes);
+    auto load_w = [&](const At& c, int st, int s) {
+      if (one) {
         mbar_arrive_expect_tx(&full[s], kWTile + c.boxes * box_bytes + S::kScale * (1 + S::kSub));
         tma_load_2d(sW + s * kWTile, &wmap, &full[s], st * kRowBytes, c.w);
         tma_load_2d(sSW + s * S::kScale, &swmap, &full[s], st * (S::kScale / 8), c.sw);
-      };
-      auto load_x = [&](const At& c, int st, int s) {
+      }
+    };
+    auto load_x = [&](const At& c, int st, int s) {
+      if (one) {
         for (int j = 0; j < c.boxes; j++)
           tma_load_2d(sX + s * S::kXTile + j * box_bytes, &xmap, &full[s], st * kRowBytes,
                       c.x + j * a.box);
         tma_load_2d(sSX + s * S::kSub * S::kScale, &sxmap, &full[s], st * (S::kScale / 8), c.sx);
-      };
-      TileAt t;
-      int e = 0;
-      // the first tile's first stages: their weights do not wait for X
-      int ahead = 0;
-      if (item0 < items) {
-        tile_at<NT>(a, s_pre, item0, &e, &t);
-        const At c = at_of(t);
-        for (; ahead < min(nst, S::kStages); ahead++) load_w(c, st_lo + ahead, ahead);
       }
-      wait_for_x();
-      int it = 0;
-      for (int item = item0; item < items && !s_fail; item += step) {
-        tile_at<NT>(a, s_pre, item, &e, &t);
-        const At c = at_of(t);
-        for (int st = st_lo; st < st_hi; st++, it++) {
-          const int s = it % S::kStages;
-          if (it >= ahead) {
-            if (it >= S::kStages && !mbar_wait(&empty[s], ((it / S::kStages) - 1) & 1)) {
-              s_fail = 1;
-              break;
-            }
-            load_w(c, st, s);
-          }
-          load_x(c, st, s);
-        }
-        if (SPLIT) break;
-      }
-      // the last copies have landed before the CTA can exit (bounded)
-      for (int j = it > S::kStages ? it - S::kStages : 0; j < it; j++)
-        if (!mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1)) { s_fail = 1; break; }
+    };
+    TileAt t;
+    int e = 0;
+    // the first tile's first stages: their weights do not wait for X
+    int ahead = 0;
+    if (item0 < items) {
+      tile_at<NT, S::kTileRows>(a, s_pre, item0, &e, &t);
+      const At c = at_of(t);
+      for (; ahead < min(nst, S::kStages); ahead++) load_w(c, st_lo + ahead, ahead);
     }
+    wait_for_x();
+    int it = 0;
+    bool ok = true;
+    Ring<S::kStages> ring;
+    for (int item = item0; item < items && ok; item += step) {
+      tile_at<NT, S::kTileRows>(a, s_pre, item, &e, &t);
+      const At c = at_of(t);
+      for (int st = st_lo; st < st_hi; st++, it++, ring.next()) {
+        if (it >= ahead) {
+          if (it >= S::kStages) ok = warp_wait(&empty[ring.s], ring.phase ^ 1);
+          if (!ok) break;
+          load_w(c, st, ring.s);
+        }
+        load_x(c, st, ring.s);
+      }
+      if (SPLIT) break;
+    }
+    // the last copies have landed before the CTA can exit (bounded)
+    for (int j = it > S::kStages ? it - S::kStages : 0; j < it && ok; j++)
+      ok = warp_wait(&full[j % S::kStages], (j / S::kStages) & 1);
+    if (!ok) s_fail = 1;
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (!TWO || crank == 0) {
+      const bool one = elect_one();
       const int steps_all = (a.K + 63) / 64;
       // addresses in 16-byte units, as descriptors hold them
       const uint32_t w_lo = smem_u32(sW) >> 4, x_lo = smem_u32(sX) >> 4;
       TileAt t;
-      int e = 0, it = 0, i = 0;
-      for (int item = item0; item < items && !s_fail; item += step, i++) {
-        tile_at<NT>(a, s_pre, item, &e, &t);
+      Ring<S::kStages> ring;
+      int e = 0, i = 0;
+      bool ok = true;
+      for (int item = item0; item < items && ok; item += step, i++) {
+        tile_at<NT, S::kTileRows>(a, s_pre, item, &e, &t);
         const int b = i % TM::kBufs;
         // the accumulator's previous tile has been read out
-        if (i >= TM::kBufs && !mbar_wait(&acc_empty[b], ((i / TM::kBufs) - 1) & 1)) {
-          s_fail = 1;
-          break;
-        }
+        if (i >= TM::kBufs) ok = warp_wait(&acc_empty[b], ((i / TM::kBufs) - 1) & 1);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(b * NT);
         // A 64-token tile may start in the middle of its scale band, two
         // columns on.  A scale address must be even, so 32-token tiles are
         // only used where a group has a single one (mx_plan).
         const uint32_t shift = NT == 64 ? (uint32_t)(t.local % 128) / 32 : 0u;
-        const uint32_t idesc = mx_idesc<FMT>((t.count + 15) & ~15);
-        bool ok = true;
-        for (int st = st_lo; st < st_hi; st++, it++) {
-          const int s = it % S::kStages;
-          if (!mbar_wait(&scale_full[it & 1], (it >> 1) & 1) ||
-              !mbar_wait(&full[s], (it / S::kStages) & 1)) {
-            ok = false;
-            break;
-          }
+        const uint32_t idesc = mx_idesc<FMT>(S::kTileRows, mma_n<TWO>(t.count));
+        for (int st = st_lo; st < st_hi; st++, ring.next()) {
+          // the scale warps arrive after the whole stage has landed
+          ok = warp_wait(&scale_full[ring.s], ring.phase);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sc = tmem + TM::kScale + (it & 1) * (TM::kScaleX + 16);
-          const uint32_t w0 = w_lo + s * (kWTile >> 4), x0 = x_lo + s * (S::kXTile >> 4);
+          const uint32_t sc = tmem + TM::kScale + ring.s * (TM::kScaleX + 16);
+          const uint32_t w0 = w_lo + ring.s * (kWTile >> 4);
+          const uint32_t x0 = x_lo + ring.s * (S::kXTile >> 4);
           const int steps = min(kSteps, steps_all - st * kSteps);
+          if (one) {
 #pragma unroll
-          for (int k = 0; k < kSteps; k++)
-            if (k < steps) {
-              const int atom = FMT == kMxE8m0 ? k / 2 : k;
-              const int id = FMT == kMxE8m0 ? (k & 1) * 2 : 0;
-              mma_mx<FMT>(d, code_desc(w0 + 2 * k), code_desc(x0 + 2 * k),
-                          idesc | ((uint32_t)id << 4) | ((uint32_t)id << 29),
-                          sc + TM::kScaleX + 4 * atom, sc + 4 * S::kSub * atom + shift,
-                          (st > st_lo || k > 0) ? 1u : 0u);
-            }
-          mma_commit(&empty[s]);
+            for (int k = 0; k < kSteps; k++)
+              if (k < steps) {
+                const int atom = FMT == kMxE8m0 ? k / 2 : k;
+                const int id = FMT == kMxE8m0 ? (k & 1) * 2 : 0;
+                mma_mx<FMT, TWO>(d, code_desc(w0 + 2 * k), code_desc(x0 + 2 * k),
+                                 idesc | ((uint32_t)id << 4) | ((uint32_t)id << 29),
+                                 sc + TM::kScaleX + 4 * atom, sc + 4 * S::kSub * atom + shift,
+                                 (st > st_lo || k > 0) ? 1u : 0u);
+              }
+            commit_mx<TWO>(&empty[ring.s]);
+          }
+          __syncwarp();
         }
-        if (!ok) { s_fail = 1; break; }
-        mma_commit(&acc_full[b]);
+        if (!ok) break;
+        if (one) commit_mx<TWO>(&acc_full[b]);
+        __syncwarp();
         if (SPLIT) break;
       }
+      if (!ok) s_fail = 1;
     }
   } else if (warp < kEpiWarp) {
     // scale tiles -> tensor memory: lane l's 16 bytes of a tile are the words
     // of its rows l, l + 32, l + 64, l + 96, four consecutive columns
     const uint32_t quadrant = (uint32_t)((warp & 3) * 32) << 16;
-    int it = 0;
+    Ring<S::kStages> ring;
     bool ok = true;
     for (int item = item0; item < items && ok; item += step) {
-      for (int st = st_lo; st < st_hi; st++, it++) {
-        const int s = it % S::kStages;
-        // the tile has landed, and the MMAs that read these columns (two
-        // stages ago) are complete
-        ok = mbar_wait(&full[s], (it / S::kStages) & 1);
-        if (ok && it >= 2)
-          ok = mbar_wait(&empty[(it - 2) % S::kStages], ((it - 2) / S::kStages) & 1);
-        ok = __all_sync(0xffffffffu, ok);
+      for (int st = st_lo; st < st_hi; st++, ring.next()) {
+        const int s = ring.s;
+        // the stage's tiles have landed, so the MMAs that read its columns the
+        // last time are complete
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ring.phase));
         if (!ok) {
           s_fail = 1;
           break;
@@ -409,13 +494,13 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
             o[0] = u.x; o[1] = u.y; o[2] = u.z; o[3] = u.w;
           }
         }
-        const uint32_t sc = tmem + TM::kScale + (it & 1) * (TM::kScaleX + 16) + quadrant;
+        const uint32_t sc = tmem + TM::kScale + s * (TM::kScaleX + 16) + quadrant;
         tmem_st<4 * S::kAtoms * S::kSub>(sc, rx);
         tmem_st<4 * S::kAtoms>(sc + TM::kScaleX, rw);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&scale_full[it & 1]);
+        if (lane == 0) arrive_first<TWO>(&scale_full[s]);
       }
       if (SPLIT) break;
     }
@@ -430,9 +515,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     TileAt t;
     int e = 0, i = 0;
     for (int item = item0; item < items; item += step, i++) {
-      tile_at<NT>(a, s_pre, item, &e, &t);
+      tile_at<NT, S::kTileRows>(a, s_pre, item, &e, &t);
       const int b = i % TM::kBufs;
-      const int n = t.n0 + q * 32 + lane;
+      const int n = t.n0 + wrow + q * 32 + lane;
       const bool nok = n < a.N;
       const int mine = t.count - part * NC;  // this warp's tokens
       float gw = 1.0f;
@@ -481,7 +566,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         if (c0 + CH == NC) {  // the accumulator's last columns are in registers
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[b]);
+          if (lane == 0) arrive_first<TWO>(&acc_empty[b]);
         }
         if (FMT == kMxE4m3) {
 #pragma unroll
@@ -539,17 +624,22 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if (TWO) cluster_sync_all();  // neither CTA's memory is in use by the other
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(TM::kCols));
+    if (TWO)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(TM::kCols));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(TM::kCols));
   }
   if (SPLIT) {
     TileAt t;
     int e = 0;
     const bool have = item0 < items;  // the same for the whole cluster
-    if (have) tile_at<NT>(a, s_pre, item0, &e, &t);
+    if (have) tile_at<NT, S::kTileRows>(a, s_pre, item0, &e, &t);
     cluster_sync_all();  // every CTA's partial is in its shared memory
     if (have) {
       const float* P = reinterpret_cast<const float*>(base);
@@ -611,23 +701,24 @@ cudaError_t make_maps(const MxTensor& x, const MxTensor& w, const MxPlan& p, int
   return e;
 }
 
-template <int FMT, int NT, bool SPLIT>
-cudaError_t launch_t(const Maps& m, const MxGemmArgs& a,
-                     const MxPlan& p, bool overlap, cudaStream_t st) {
-  constexpr int smem = Shape<FMT, NT>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<FMT, NT, SPLIT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <int FMT, int NT, int MODE>
+cudaError_t launch_t(const Maps& m, const MxGemmArgs& a, const MxPlan& p, bool overlap,
+                     cudaStream_t st) {
+  using S = Shape<FMT, NT, MODE>;
+  cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<FMT, NT, MODE>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = SPLIT ? dim3((unsigned)p.split, (unsigned)p.tiles, 1) : dim3((unsigned)p.ctas, 1, 1);
-  cfg.blockDim = dim3(Shape<FMT, NT>::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = MODE == kSplit ? dim3((unsigned)p.split, (unsigned)p.tiles, 1)
+                               : dim3((unsigned)p.ctas, 1, 1);
+  cfg.blockDim = dim3(S::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   int n = 0;
-  if (SPLIT) {
+  if (MODE != kWalk) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = (unsigned)p.split;
+    attr[n].val.clusterDim.x = MODE == kSplit ? (unsigned)p.split : 2u;
     attr[n].val.clusterDim.y = 1;
     attr[n].val.clusterDim.z = 1;
     n++;
@@ -639,26 +730,26 @@ cudaError_t launch_t(const Maps& m, const MxGemmArgs& a,
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NT, SPLIT>, m.x, m.w, m.sx, m.sw, a);
+  return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NT, MODE>, m.x, m.w, m.sx, m.sw, a);
+}
+
+template <int FMT, int MODE>
+cudaError_t launch_m(const Maps& m, const MxGemmArgs& a, const MxPlan& p, bool overlap,
+                     cudaStream_t st) {
+  switch (p.nt) {
+    case 32: return launch_t<FMT, 32, MODE>(m, a, p, overlap, st);
+    case 64: return launch_t<FMT, 64, MODE>(m, a, p, overlap, st);
+    case 128: return launch_t<FMT, 128, MODE>(m, a, p, overlap, st);
+    default: return launch_t<FMT, 256, MODE>(m, a, p, overlap, st);
+  }
 }
 
 template <int FMT>
-cudaError_t launch_f(const Maps& m, const MxGemmArgs& a,
-                     const MxPlan& p, bool overlap, cudaStream_t st) {
-  if (p.split > 1) {
-    switch (p.nt) {
-      case 32: return launch_t<FMT, 32, true>(m, a, p, overlap, st);
-      case 64: return launch_t<FMT, 64, true>(m, a, p, overlap, st);
-      case 128: return launch_t<FMT, 128, true>(m, a, p, overlap, st);
-      default: return launch_t<FMT, 256, true>(m, a, p, overlap, st);
-    }
-  }
-  switch (p.nt) {
-    case 32: return launch_t<FMT, 32, false>(m, a, p, overlap, st);
-    case 64: return launch_t<FMT, 64, false>(m, a, p, overlap, st);
-    case 128: return launch_t<FMT, 128, false>(m, a, p, overlap, st);
-    default: return launch_t<FMT, 256, false>(m, a, p, overlap, st);
-  }
+cudaError_t launch_f(const Maps& m, const MxGemmArgs& a, const MxPlan& p, bool overlap,
+                     cudaStream_t st) {
+  if (p.pair) return launch_t<FMT, 256, kPair>(m, a, p, overlap, st);
+  return p.split > 1 ? launch_m<FMT, kSplit>(m, a, p, overlap, st)
+                     : launch_m<FMT, kWalk>(m, a, p, overlap, st);
 }
 
 }  // namespace
@@ -676,6 +767,19 @@ MxPlan mx_plan(int groups, int64_t rows, int64_t N, int64_t K) {
   if (c > 8) c = 8;
   if (c > stages) c = stages;
   p.split = c < 1 ? 1 : (int)c;
+  p.pair = 0;
+  if (p.nt == 256) {
+    const int64_t n2 = (N + 2 * kWRows - 1) / (2 * kWRows);
+    const int64_t t2 = groups == 1 ? (rows + 255) / 256 * n2 : (rows / 256 + busy) * n2;
+    if (t2 >= kSms / 2) {
+      p.pair = 1;
+      p.split = 1;
+      p.tiles = t2;
+      p.ctas = kSms;
+      p.stages = (int)stages;
+      return p;
+    }
+  }
   p.ctas = (int)(p.split > 1 ? p.tiles * p.split : (p.tiles < kSms ? p.tiles : kSms));
   p.stages = (int)stages;
   return p;
@@ -687,13 +791,13 @@ cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f
   const MxPlan p = mx_plan(x.groups, x.rows, N, x.K);
   // One copy for all of a tile's token rows; ragged groups leave many tiles
   // part empty and take pieces, of which only those with rows are fetched.
-  const int box = x.groups == 1 ? p.nt : (p.nt < 128 ? 32 : 64);
+  const int box = x.groups == 1 ? (p.pair ? p.nt / 2 : p.nt) : (p.nt < 128 ? 32 : 64);
   Maps m;
   const cudaError_t e = make_maps(x, w, p, box, &m);
   if (e != cudaSuccess) return e;
   const MxGemmArgs a{x.row_scale, w.row_scale, Y, ldy,
                      MxRows{x.offsets, x.groups, (int)x.rows}, (int)N, (int)x.K,
-                     (int)((N + kWRows - 1) / kWRows), p.stages, box, f32 ? 0 : 1};
+                     (int)((N + kWRows - 1) / kWRows + p.pair) / (1 + p.pair), p.stages, box, f32 ? 0 : 1};
   return x.fmt == kMxE8m0 ? launch_f<kMxE8m0>(m, a, p, overlap, st)
                           : launch_f<kMxE4m3>(m, a, p, overlap, st);
 }

@@ -435,10 +435,11 @@ aaac_status aaac_mx_linear_ws(const aaac_mx_source* src, int64_t rows, const int
                               void* ws, size_t ws_bytes, void* stream);
 
 /* The product's plan for `rows` rows in `groups` groups, N weight rows per
- * group and K columns.  A host-only query.  out (host int32[5]):
+ * group and K columns.  A host-only query.  out (host int32[6]):
  *   out[0]  token columns of a tile      out[1]  CTAs that share a tile's K
  *   out[2]  CTAs                         out[3]  256-column stages of K
- *   out[4]  output tiles (an upper bound when there is more than one group) */
+ *   out[4]  output tiles (an upper bound when there is more than one group)
+ *   out[5]  weight rows of a tile: 128, or 256 for two CTAs together */
 aaac_status aaac_mx_launch_plan(int32_t groups, int64_t rows, int64_t N, int64_t K, int32_t* out);
 
 /* Device-side wait status of the current device: *flag = 1 when a bounded

@@ -164,7 +164,8 @@ def test_plan_covers_every_split_of_the_rows(lib, groups, rows, N, K):
     p = bb.mx_launch_plan(groups, rows, N, K)
     assert p["stages"] == -(-K // 256)
     assert 1 <= p["split"] <= min(8, p["stages"])
-    n_tiles = -(-N // 128)
+    assert p["rows"] in (128, 256) and (p["rows"] == 128 or p["split"] == 1)
+    n_tiles = -(-N // p["rows"])
     assert p["columns"] in (32, 64, 128, 256)
     # a 32-token tile may not start inside a scale band: one such tile a group
     assert p["columns"] > 32 or (groups == 1 and rows <= 32)
@@ -181,7 +182,7 @@ def test_plan_covers_every_split_of_the_rows(lib, groups, rows, N, K):
 
 
 def test_plan_refusals(lib):
-    out = (ctypes.c_int32 * 5)()
+    out = (ctypes.c_int32 * 6)()
     assert lib.aaac_mx_launch_plan(1, 4, 4, 64, None) == INVALID
     for args in ((0, 4, 4, 64), (1, 0, 4, 64), (1, 4, 0, 64), (1, 4, 4, 48),
                  (1, (1 << 31) - 1, (1 << 31) - 1, 64)):
