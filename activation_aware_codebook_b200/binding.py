@@ -552,7 +552,7 @@ class MxTensor:
         if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous():
             raise ValueError("codes must be contiguous uint8 [rows, K/2]")
         rows, half = codes.shape
-        need = _mx_bytes(load().aaac_mx_scale_bytes, fmt, rows, 2 * half, groups)
+        need = _mx_bytes((_lib or load()).aaac_mx_scale_bytes, fmt, rows, 2 * half, groups)
         if scales.dtype != torch.uint8 or scales.numel() < need or not scales.is_contiguous():
             raise ValueError(f"scales must be contiguous uint8, {need} bytes")
         if fmt != MX_E4M3:
@@ -562,7 +562,7 @@ class MxTensor:
             raise ValueError(f"row_scale must be contiguous float32 [{rows}]")
         if offsets is not None:
             _mx_offsets(offsets, groups)
-        _mx_on(codes.get_device(), codes, scales, row_scale, offsets)
+        _mx_on(codes.get_device(), scales, row_scale, offsets)
         self._set(codes, scales, row_scale, fmt, groups, offsets, rows, 2 * half)
 
     def _set(self, codes, scales, row_scale, fmt, groups, offsets, rows, K):
@@ -581,7 +581,7 @@ class MxTensor:
     @staticmethod
     def empty(fmt: int, rows: int, K: int, groups: int = 1,
               offsets: Optional[torch.Tensor] = None, device="cuda") -> "MxTensor":
-        need = _mx_bytes(load().aaac_mx_scale_bytes, fmt, rows, K, groups)
+        need = _mx_bytes((_lib or load()).aaac_mx_scale_bytes, fmt, rows, K, groups)
         if offsets is not None:
             _mx_offsets(offsets, groups)
         t = object.__new__(MxTensor)
@@ -610,6 +610,7 @@ def _mx_offsets(offsets: torch.Tensor, groups: int) -> None:
 def _mx_on(device: int, *tensors) -> None:
     """Every tensor on CUDA device `device`."""
     if device < 0:
+        _need_cuda()
         raise ValueError("libaaac takes device tensors only")
     for t in tensors:
         if t is not None and t.get_device() != device:
@@ -630,33 +631,37 @@ def _mx_stream(device: int, stream) -> int:
 def _on_stream(f, stream, *args):
     """f(*args), its own allocations made on `stream` (the caching allocator
     ties memory to the stream it was allocated on)."""
-    if stream is None:
-        return f(*args)
     with torch.cuda.stream(stream):
         return f(*args)
 
 
 def _mx_source(X: torch.Tensor, rows: Optional[torch.Tensor], swiglu: bool):
     """(aaac_mx_source, quantised rows, K, the tensor it points into)."""
-    if X.dtype not in _MX_TYPES or X.dim() != 2:
+    kind = _MX_TYPES.get(X.dtype)
+    if kind is None or X.dim() != 2:
         raise ValueError("X must be a bfloat16 or float32 matrix")
-    if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1
-                             or not rows.is_contiguous()):
-        raise ValueError("rows must be contiguous int32 [quantised rows]")
     n, width = X.shape
     ldx, step = X.stride()
-    if step != 1 or ldx * X.element_size() % 16 or ldx < width or X.data_ptr() % 16:
+    at = X.data_ptr()
+    # 16-byte aligned rows: 8 bf16 or 4 fp32 values
+    if step != 1 or ldx % (4 if kind else 8) or ldx < width or at % 16:
         X = X.contiguous()
-        ldx = width
-    src = CMxSource(X.data_ptr(), _MX_TYPES[X.dtype], MX_SWIGLU if swiglu else 0, n, ldx,
-                    None if rows is None else rows.data_ptr())
-    return src, n if rows is None else rows.numel(), width // 2 if swiglu else width, X
+        ldx, at = width, X.data_ptr()
+    if rows is None:
+        index, out_rows = None, n
+    else:
+        if rows.dtype != torch.int32 or rows.dim() != 1 or not rows.is_contiguous():
+            raise ValueError("rows must be contiguous int32 [quantised rows]")
+        index, out_rows = rows.data_ptr(), rows.numel()
+    if swiglu:
+        return CMxSource(at, kind, MX_SWIGLU, n, ldx, index), out_rows, width // 2, X
+    return CMxSource(at, kind, 0, n, ldx, index), out_rows, width, X
 
 
-def _mx_out(out: Optional[torch.Tensor], rows: int, cols: int, dtype, like: torch.Tensor):
+def _mx_out(out: Optional[torch.Tensor], rows: int, cols: int, dtype, device):
     """(output, its aaac_type, its leading dimension)."""
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=like.device), _MX_TYPES[dtype], cols
+        return torch.empty((rows, cols), dtype=dtype, device=device), _MX_TYPES[dtype], cols
     if (out.shape != (rows, cols) or out.dtype not in _MX_TYPES
             or (cols > 1 and out.stride(1) != 1)):
         raise ValueError(f"out must be a bfloat16 or float32 [{rows}, {cols}] with "
@@ -672,36 +677,40 @@ def mx_quantize(X: torch.Tensor, fmt: int, rows: Optional[torch.Tensor] = None,
     (int32) picks the source row of each quantised row (-1: a row of zeros);
     swiglu quantises silu(a) * b of X's two halves [n, 2K]; groups and offsets
     are the rows' groups (see MxTensor)."""
-    _need_cuda()
-    return _on_stream(_mx_quantize, stream, X, fmt, rows, swiglu, groups, offsets, out, stream)
+    if stream is not None:
+        return _on_stream(_mx_quantize, stream, X, fmt, rows, swiglu, groups, offsets, out, stream)
+    return _mx_quantize(X, fmt, rows, swiglu, groups, offsets, out, None)
 
 
 def _mx_quantize(X, fmt, rows, swiglu, groups, offsets, out, stream):
     src, n, K, X = _mx_source(X, rows, swiglu)
     device = X.get_device()
-    at = _mx_stream(device, stream)
     if out is None:
+        _mx_on(device, rows, offsets)
         out = MxTensor.empty(fmt, n, K, groups, offsets, X.device)
-    elif (out.fmt, out.rows, out.K) != (fmt, n, K):
-        raise ValueError(f"out is fmt {out.fmt} [{out.rows}, {out.K}], not {fmt} [{n}, {K}]")
-    _mx_on(device, rows, out.codes, offsets)
-    _check(load().aaac_mx_quantize(ctypes.byref(src), out._ref, at))
+    else:
+        if (out.fmt, out.rows, out.K) != (fmt, n, K):
+            raise ValueError(f"out is fmt {out.fmt} [{out.rows}, {out.K}], not {fmt} [{n}, {K}]")
+        _mx_on(device, rows, out.codes)
+    _check((_lib or load()).aaac_mx_quantize(ctypes.byref(src), out._ref,
+                                             _mx_stream(device, stream)))
     return out
 
 
 def mx_dequant(q: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
     """A microscaled tensor's values, bf16 or fp32 [rows, K]."""
-    _need_cuda()
-    return _on_stream(_mx_dequant, stream, q, dtype, out, stream)
+    if stream is not None:
+        return _on_stream(_mx_dequant, stream, q, dtype, out, stream)
+    return _mx_dequant(q, dtype, out, None)
 
 
 def _mx_dequant(q, dtype, out, stream):
     device = q.codes.get_device()
-    at = _mx_stream(device, stream)
-    out, kind, ld = _mx_out(out, q.rows, q.K, dtype, q.codes)
+    out, kind, ld = _mx_out(out, q.rows, q.K, dtype, q.codes.device)
     _mx_on(device, out)
-    _check(load().aaac_mx_dequant(q._ref, out.data_ptr(), kind, ld, at))
+    _check((_lib or load()).aaac_mx_dequant(q._ref, out.data_ptr(), kind, ld,
+                                            _mx_stream(device, stream)))
     return out
 
 
@@ -714,41 +723,48 @@ def mx_linear(X: Union[torch.Tensor, MxTensor], W: MxTensor, out: Optional[torch
     microscaled tensor, or bf16 / fp32 activations that are quantised here as
     mx_quantize does (rows, swiglu and offsets as there; ws: a workspace of
     mx_workspace_size bytes)."""
-    _need_cuda()
     if isinstance(X, MxTensor):
         if rows is not None or swiglu or offsets is not None or ws is not None:
             raise ValueError("rows, swiglu, offsets and ws go with activations that are not "
                              "quantised yet")
-        return _on_stream(_mx_product, stream, X, W, out, out_dtype, stream)
-    return _on_stream(_mx_linear, stream, X, W, out, out_dtype, rows, swiglu, offsets, ws, stream)
+        if stream is not None:
+            return _on_stream(_mx_product, stream, X, W, out, out_dtype, stream)
+        return _mx_product(X, W, out, out_dtype, None)
+    if stream is not None:
+        return _on_stream(_mx_linear, stream, X, W, out, out_dtype, rows, swiglu, offsets, ws,
+                          stream)
+    return _mx_linear(X, W, out, out_dtype, rows, swiglu, offsets, ws, None)
 
 
 def _mx_product(X, W, out, out_dtype, stream):
     device = X.codes.get_device()
-    at = _mx_stream(device, stream)
-    out, kind, ld = _mx_out(out, X.rows, W.rows // W.groups, out_dtype, X.codes)
+    out, kind, ld = _mx_out(out, X.rows, W.rows // W.groups, out_dtype, X.codes.device)
     _mx_on(device, W.codes, out)
-    _check(load().aaac_mx_linear(X._ref, W._ref, out.data_ptr(), kind, ld, at))
+    _check((_lib or load()).aaac_mx_linear(X._ref, W._ref, out.data_ptr(), kind, ld,
+                                           _mx_stream(device, stream)))
     return out
 
 
 def _mx_linear(X, W, out, out_dtype, rows, swiglu, offsets, ws, stream):
     src, n, K, X = _mx_source(X, rows, swiglu)
     device = X.get_device()
-    at = _mx_stream(device, stream)
     if K != W.K:
         raise ValueError(f"X has K={K}, W has K={W.K}")
+    _mx_on(device, W.codes, rows, offsets, out, ws)
     if offsets is not None:
         _mx_offsets(offsets, W.groups)
-    out, kind, ld = _mx_out(out, n, W.rows // W.groups, out_dtype, X)
+    where = X.device
+    out, kind, ld = _mx_out(out, n, W.rows // W.groups, out_dtype, where)
+    lib = _lib or load()
     if ws is None:
-        need = _mx_bytes(load().aaac_mx_workspace_size, W.fmt, n, K, W.groups)
-        ws = torch.empty(need, dtype=torch.uint8, device=X.device)
-    _mx_on(device, rows, offsets, W.codes, out, ws)
-    _check(load().aaac_mx_linear_ws(ctypes.byref(src), n,
-                                    None if offsets is None else offsets.data_ptr(), W._ref,
-                                    out.data_ptr(), kind, ld, ws.data_ptr(),
-                                    ws.numel() * ws.element_size(), at))
+        size = _mx_bytes(lib.aaac_mx_workspace_size, W.fmt, n, K, W.groups)
+        ws = torch.empty(size, dtype=torch.uint8, device=where)
+    else:
+        size = ws.numel() * ws.element_size()
+    _check(lib.aaac_mx_linear_ws(ctypes.byref(src), n,
+                                 None if offsets is None else offsets.data_ptr(), W._ref,
+                                 out.data_ptr(), kind, ld, ws.data_ptr(), size,
+                                 _mx_stream(device, stream)))
     return out
 
 
