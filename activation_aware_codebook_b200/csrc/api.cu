@@ -811,7 +811,7 @@ aaac_status aaac_mx_launch_plan(int32_t groups, int64_t rows, int64_t N, int64_t
   if (rows < 1 || N < 1 || N > INT32_MAX || (rows / 32 + groups) * ((N + 127) / 128) > INT32_MAX)
     return fail(AAAC_ERR_SHAPE, "rows=%lld or N=%lld out of range", (long long)rows, (long long)N);
   const aaac::MxPlan p = aaac::mx_plan(groups, rows, N, K);
-  out[0] = p.nt;
+  out[0] = p.width;
   out[1] = p.split;
   out[2] = p.ctas;
   out[3] = p.stages;

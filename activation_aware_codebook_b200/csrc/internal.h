@@ -155,7 +155,8 @@ struct MxTensor {
   int64_t rows, K;
 };
 struct MxPlan {
-  int nt;         // token columns of a tile
+  int nt;         // token columns of the kernel's tiles
+  int width;      // tokens taken to a tile
   int split;      // CTAs that share a tile's K (1: persistent CTAs over the tiles)
   int pair;       // 1: two CTAs to a tile of 256 weight rows
   int ctas;

@@ -25,6 +25,8 @@
 // tiles in rank order through distributed shared memory: the sum's order is
 // fixed, whatever the timing.
 // Waits are bounded (tcgen05.cuh); a CTA that gives up writes NaN.
+#include <math.h>
+
 #include "common.cuh"
 #include "internal.h"
 #include "mx.cuh"
@@ -35,13 +37,14 @@ namespace aaac {
 namespace {
 
 constexpr int kWRows = 128;        // weight rows of a tile (MMA M)
+constexpr int kEpiWarp = 6;        // the first epilogue warp
 constexpr int kStageK = 256;       // columns of a stage
 constexpr int kRowBytes = 128;     // of packed codes per stage and row
 constexpr int kSteps = 4;          // MMAs of K = 64 per stage
-constexpr int kEpiWarp = 6;        // the first epilogue warp
 constexpr int kWTile = kWRows * kRowBytes;  // 16 KB
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kSms = 148;
+constexpr int kMaxSplit = 8;       // CTAs that share a tile's K
 
 struct MxGemmArgs {
   const float* gx;
@@ -52,6 +55,7 @@ struct MxGemmArgs {
   int N, K;
   int n_tiles;        // weight tiles per group
   int stages;         // ceil(K / 256)
+  int width;          // tokens of a tile: NT, or fewer
   int box;            // token rows of one TMA copy
   int bf16_out;
 };
@@ -65,7 +69,7 @@ template <int FMT, int NT, int MODE>
 struct Shape {
   static constexpr bool kTwo = MODE == kPair;
   static constexpr int kTileRows = kTwo ? 2 * kWRows : kWRows;  // weight rows of a tile
-  static constexpr int kSub = (NT + 127) / 128;             // 128-row scale bands of a token tile
+  static constexpr int kSub = (NT + 127) / 128;             // 128-row scale bands a token tile meets
   static constexpr int kAtoms = FMT == kMxE8m0 ? 2 : 4;     // scale tiles of a stage along K
   static constexpr int kScale = kAtoms * kMxTileBytes;      // of one band
   static constexpr int kXTile = (kTwo ? NT / 2 : NT) * kRowBytes;  // a pair's CTAs hold half each
@@ -178,6 +182,17 @@ __device__ __forceinline__ void wait_for_x() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+__device__ __forceinline__ float4 ld_cluster_f4(const float* local, uint32_t rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
 // Columns of tensor memory to registers, without waiting.
 __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -234,7 +249,7 @@ __device__ __forceinline__ int mma_n(int count) {
 
 // Tile `item`, one of the s_pre[groups] * n_tiles; *e (the search's start) only
 // moves forward.
-template <int NT, int ROWS>
+template <int ROWS>
 __device__ __forceinline__ void tile_at(const MxGemmArgs& a, const int* s_pre, int item, int* e,
                                         TileAt* t) {
   while (item >= s_pre[*e + 1] * a.n_tiles) (*e)++;
@@ -244,9 +259,9 @@ __device__ __forceinline__ void tile_at(const MxGemmArgs& a, const int* s_pre, i
   mx_group(a.rows, *e, &t->first, &last);
   t->e = *e;
   t->n0 = (at / tt) * ROWS;
-  t->local = (at % tt) * NT;
+  t->local = (at % tt) * a.width;
   t->row = t->first + t->local;
-  t->count = min(NT, last - t->row);
+  t->count = min(a.width, last - t->row);
 }
 
 template <int FMT, int NT, int MODE>
@@ -282,7 +297,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   for (int e = threadIdx.x; e < a.rows.groups; e += S::kThreads) {
     int first, last;
     mx_group(a.rows, e, &first, &last);
-    s_pre[e + 1] = (last - first + NT - 1) / NT;
+    s_pre[e + 1] = (last - first + a.width - 1) / a.width;
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; s++) {
@@ -384,7 +399,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     // the first tile's first stages: their weights do not wait for X
     int ahead = 0;
     if (item0 < items) {
-      tile_at<NT, S::kTileRows>(a, s_pre, item0, &e, &t);
+      tile_at<S::kTileRows>(a, s_pre, item0, &e, &t);
       const At c = at_of(t);
       for (; ahead < min(nst, S::kStages); ahead++) load_w(c, st_lo + ahead, ahead);
     }
@@ -393,7 +408,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     bool ok = true;
     Ring<S::kStages> ring;
     for (int item = item0; item < items && ok; item += step) {
-      tile_at<NT, S::kTileRows>(a, s_pre, item, &e, &t);
+      tile_at<S::kTileRows>(a, s_pre, item, &e, &t);
       const At c = at_of(t);
       for (int st = st_lo; st < st_hi; st++, it++, ring.next()) {
         if (it >= ahead) {
@@ -420,17 +435,17 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       int e = 0, i = 0;
       bool ok = true;
       for (int item = item0; item < items && ok; item += step, i++) {
-        tile_at<NT, S::kTileRows>(a, s_pre, item, &e, &t);
+        tile_at<S::kTileRows>(a, s_pre, item, &e, &t);
         const int b = i % TM::kBufs;
         // the accumulator's previous tile has been read out
         if (i >= TM::kBufs) ok = warp_wait(&acc_empty[b], ((i / TM::kBufs) - 1) & 1);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(b * NT);
-        // A 64-token tile may start in the middle of its scale band, two
-        // columns on.  A scale address must be even, so 32-token tiles are
-        // only used where a group has a single one (mx_plan).
-        const uint32_t shift = NT == 64 ? (uint32_t)(t.local % 128) / 32 : 0u;
+        // Tiles of 64 or 192 tokens may start in the middle of a scale band,
+        // two columns on.  A scale address must be even, so 32-token tiles
+        // are only used where there is a single one (mx_plan).
+        const uint32_t shift = (uint32_t)(t.local % 128) / 32;
         const uint32_t idesc = mx_idesc<FMT>(S::kTileRows, mma_n<TWO>(t.count));
         for (int st = st_lo; st < st_hi; st++, ring.next()) {
           // the scale warps arrive after the whole stage has landed
@@ -515,7 +530,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     TileAt t;
     int e = 0, i = 0;
     for (int item = item0; item < items; item += step, i++) {
-      tile_at<NT, S::kTileRows>(a, s_pre, item, &e, &t);
+      tile_at<S::kTileRows>(a, s_pre, item, &e, &t);
       const int b = i % TM::kBufs;
       const int n = t.n0 + wrow + q * 32 + lane;
       const bool nok = n < a.N;
@@ -639,22 +654,60 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     TileAt t;
     int e = 0;
     const bool have = item0 < items;  // the same for the whole cluster
-    if (have) tile_at<NT, S::kTileRows>(a, s_pre, item0, &e, &t);
+    if (have) tile_at<S::kTileRows>(a, s_pre, item0, &e, &t);
     cluster_sync_all();  // every CTA's partial is in its shared memory
     if (have) {
+      // Four weight rows of a token at a time: one 16-byte read of every CTA's
+      // partial, all in flight before the first sum, added in rank order.
       const float* P = reinterpret_cast<const float*>(base);
-      const int E = t.count * kWRows;
+      const int E = t.count * (kWRows / 4);
       const int e0 = (int)((int64_t)crank * E / csize), e1 = (int)((int64_t)(crank + 1) * E / csize);
+      const int size_y = a.bf16_out ? 2 : 4;
+      const bool wide = reinterpret_cast<uintptr_t>(a.Y) % (4 * size_y) == 0 && a.ldy % 4 == 0;
       for (int i = e0 + threadIdx.x; i < e1; i += S::kThreads) {
-        const int c = i / kWRows, n = t.n0 + i % kWRows;
-        if (n < a.N) {
-          float v = 0.0f;
-          for (uint32_t k = 0; k < csize; k++) v = __fadd_rn(v, ld_cluster_f32(P + i, k));
-          if (FMT == kMxE4m3)
-            v = __fmul_rn(__fmul_rn(v, __ldg(a.gx + t.row + c)), __ldg(a.gw + (int64_t)t.e * a.N + n));
-          const int64_t y = (int64_t)(t.row + c) * a.ldy + n;
-          if (a.bf16_out) static_cast<__nv_bfloat16*>(a.Y)[y] = __float2bfloat16_rn(v);
-          else static_cast<float*>(a.Y)[y] = v;
+        const int c = i / (kWRows / 4), n = t.n0 + i % (kWRows / 4) * 4;
+        float4 part[kMaxSplit];
+#pragma unroll
+        for (int k = 0; k < kMaxSplit; k++)
+          if (k < (int)csize) part[k] = ld_cluster_f4(P + 4 * i, (uint32_t)k);
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < kMaxSplit; k++)
+          if (k < (int)csize) {
+            v[0] = __fadd_rn(v[0], part[k].x);
+            v[1] = __fadd_rn(v[1], part[k].y);
+            v[2] = __fadd_rn(v[2], part[k].z);
+            v[3] = __fadd_rn(v[3], part[k].w);
+          }
+        if (FMT == kMxE4m3) {
+          const float g = __ldg(a.gx + t.row + c);
+          const float* gw = a.gw + (int64_t)t.e * a.N;
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+            v[j] = __fmul_rn(__fmul_rn(v[j], g), n + j < a.N ? __ldg(gw + n + j) : 0.0f);
+        }
+        const int64_t y = (int64_t)(t.row + c) * a.ldy + n;
+        if (a.bf16_out) {
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.Y) + y;
+          if (wide && n + 3 < a.N) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(v[2], v[3]);
+            *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                      *reinterpret_cast<const uint32_t*>(&hi));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+              if (n + j < a.N) o[j] = __float2bfloat16_rn(v[j]);
+          }
+        } else {
+          float* o = static_cast<float*>(a.Y) + y;
+          if (wide && n + 3 < a.N) {
+            *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+              if (n + j < a.N) o[j] = v[j];
+          }
         }
       }
     }
@@ -754,34 +807,61 @@ cudaError_t launch_f(const Maps& m, const MxGemmArgs& a, const MxPlan& p, bool o
 
 }  // namespace
 
+// The plan with the least estimated time, in microseconds as measured at
+// N = 1024 to 14336, K = 4096 to 27648 and 128 to 2048 tokens (the estimate is
+// within a tenth there): a stage of a tile takes 0.20 + 0.0011 per token
+// column, of which the first part is the weight tile's way from L2 (narrow
+// tiles pay it more often), and a tile's last stages and stores 0.5.  CTAs
+// that split a tile run one after the other where there are too many of them,
+// each with its start, and its joining of the parts, 4 for every 256 columns.
+// Pairs of CTAs take tiles of twice the weight rows in the time of single
+// ones and with a third less traffic, as soon as there are tiles for all:
+// 2048 x 14336 x 16384 takes 189 us with them and 202 without, of which 0.93.
 MxPlan mx_plan(int groups, int64_t rows, int64_t N, int64_t K) {
   MxPlan p;
-  const int64_t busy = groups < rows ? groups : rows;  // groups that can hold rows
-  const int64_t each = (rows + busy - 1) / busy;
-  p.nt = groups == 1 && rows <= 32 ? 32 : (each <= 64 ? 64 : (each <= 128 ? 128 : 256));
-  const int64_t n_tiles = (N + kWRows - 1) / kWRows;
   const int64_t stages = (K + kStageK - 1) / kStageK;
-  // an upper bound of the tiles: sum ceil(c / NT) <= rows / NT + one per busy group
-  p.tiles = groups == 1 ? (rows + p.nt - 1) / p.nt * n_tiles : (rows / p.nt + busy) * n_tiles;
-  int64_t c = kSms / p.tiles;
-  if (c > 8) c = 8;
-  if (c > stages) c = stages;
-  p.split = c < 1 ? 1 : (int)c;
-  p.pair = 0;
-  if (p.nt == 256) {
-    const int64_t n2 = (N + 2 * kWRows - 1) / (2 * kWRows);
-    const int64_t t2 = groups == 1 ? (rows + 255) / 256 * n2 : (rows / 256 + busy) * n2;
-    if (t2 >= kSms / 2) {
-      p.pair = 1;
-      p.split = 1;
-      p.tiles = t2;
-      p.ctas = kSms;
-      p.stages = (int)stages;
-      return p;
+  const int64_t n1 = (N + kWRows - 1) / kWRows, n2 = (N + 2 * kWRows - 1) / (2 * kWRows);
+  const int64_t busy = groups < rows ? groups : rows;  // groups that can hold rows
+  const double each = (double)rows / (double)busy;
+  double best = 0.0;
+  p.width = 0;
+  // token tiles: of ragged groups, half a tile more than their rows fill
+  auto token_tiles = [&](int width) {
+    if (groups == 1) return (double)((rows + width - 1) / width);
+    const double t = each / width + 0.5;
+    return (double)busy * (t > 1.0 ? t : 1.0);
+  };
+  auto offer = [&](int width, int split, bool pair) {
+    const double tt = token_tiles(width);
+    const double columns = (double)rows / tt;
+    const double tiles = tt * (double)(pair ? n2 : n1);
+    const double waves = ceil(tiles * split / (pair ? kSms / 2 : kSms));
+    const double stage = 0.20 + 0.0011 * columns;
+    const double own = (double)((stages + split - 1) / split) * stage + 0.5;
+    const double t = waves * (split > 1 ? own + 2.0 + columns / 64.0 : pair ? 0.93 * own : own);
+    if (p.width == 0 || t < best) {
+      best = t;
+      p.width = width;
+      p.split = split;
+      p.pair = pair ? 1 : 0;
+    }
+  };
+  if (groups == 1 && rows <= 32) {
+    for (int s = 1; s <= kMaxSplit && s <= stages; s++) offer(32, s, false);
+  } else {
+    for (int w = 64; w <= 256; w += 64) {
+      for (int s = 1; s <= kMaxSplit && s <= stages; s++) offer(w, s, false);
+      if (w > 128 && token_tiles(w) * (double)n2 >= kSms / 2) offer(w, 1, true);
+      if (w >= each) break;
     }
   }
-  p.ctas = (int)(p.split > 1 ? p.tiles * p.split : (p.tiles < kSms ? p.tiles : kSms));
+  p.nt = p.width > 128 ? 256 : p.width;
+  const int64_t n = p.pair ? n2 : n1;
+  // an upper bound of the tiles: sum ceil(c / width) <= rows / width + one per busy group
+  p.tiles = groups == 1 ? (rows + p.width - 1) / p.width * n : (rows / p.width + busy) * n;
+  if (p.tiles > 65535) p.split = 1;  // a grid's y
   p.stages = (int)stages;
+  p.ctas = p.pair ? kSms : (int)(p.split > 1 ? p.tiles * p.split : (p.tiles < kSms ? p.tiles : kSms));
   return p;
 }
 
@@ -791,13 +871,13 @@ cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f
   const MxPlan p = mx_plan(x.groups, x.rows, N, x.K);
   // One copy for all of a tile's token rows; ragged groups leave many tiles
   // part empty and take pieces, of which only those with rows are fetched.
-  const int box = x.groups == 1 ? (p.pair ? p.nt / 2 : p.nt) : (p.nt < 128 ? 32 : 64);
+  const int box = x.groups == 1 ? (p.pair ? p.width / 2 : p.width) : (p.nt < 128 ? 32 : 64);
   Maps m;
   const cudaError_t e = make_maps(x, w, p, box, &m);
   if (e != cudaSuccess) return e;
   const MxGemmArgs a{x.row_scale, w.row_scale, Y, ldy,
                      MxRows{x.offsets, x.groups, (int)x.rows}, (int)N, (int)x.K,
-                     (int)((N + kWRows - 1) / kWRows + p.pair) / (1 + p.pair), p.stages, box, f32 ? 0 : 1};
+                     (int)((N + kWRows - 1) / kWRows + p.pair) / (1 + p.pair), p.stages, p.width, box, f32 ? 0 : 1};
   return x.fmt == kMxE8m0 ? launch_f<kMxE8m0>(m, a, p, overlap, st)
                           : launch_f<kMxE4m3>(m, a, p, overlap, st);
 }

@@ -436,7 +436,7 @@ aaac_status aaac_mx_linear_ws(const aaac_mx_source* src, int64_t rows, const int
 
 /* The product's plan for `rows` rows in `groups` groups, N weight rows per
  * group and K columns.  A host-only query.  out (host int32[6]):
- *   out[0]  token columns of a tile      out[1]  CTAs that share a tile's K
+ *   out[0]  tokens of a tile             out[1]  CTAs that share a tile's K
  *   out[2]  CTAs                         out[3]  256-column stages of K
  *   out[4]  output tiles (an upper bound when there is more than one group)
  *   out[5]  weight rows of a tile: 128, or 256 for two CTAs together */
