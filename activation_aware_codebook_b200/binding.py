@@ -529,7 +529,8 @@ def mx_scale_bytes(fmt: int, rows: int, K: int, groups: int = 1) -> int:
 
 
 def mx_workspace_size(fmt: int, rows: int, K: int, groups: int = 1) -> int:
-    """Bytes of the workspace in which mx_linear quantises its activations."""
+    """Bytes of the workspace in which mx_linear quantises its activations (0
+    for the few rows that the product's kernel quantises itself)."""
     return int(load().aaac_mx_workspace_size(fmt, rows, K, groups))
 
 
@@ -757,13 +758,14 @@ def _mx_linear(X, W, out, out_dtype, rows, swiglu, offsets, ws, stream):
     out, kind, ld = _mx_out(out, n, W.rows // W.groups, out_dtype, where)
     lib = _lib or load()
     if ws is None:
-        size = _mx_bytes(lib.aaac_mx_workspace_size, W.fmt, n, K, W.groups)
-        ws = torch.empty(size, dtype=torch.uint8, device=where)
+        # 0: the product quantises these rows itself (or refuses the sizes below)
+        size = lib.aaac_mx_workspace_size(W.fmt, n, K, W.groups)
+        ws = torch.empty(size, dtype=torch.uint8, device=where) if size else None
     else:
         size = ws.numel() * ws.element_size()
     _check(lib.aaac_mx_linear_ws(ctypes.byref(src), n,
                                  None if offsets is None else offsets.data_ptr(), W._ref,
-                                 out.data_ptr(), kind, ld, ws.data_ptr(), size,
+                                 out.data_ptr(), kind, ld, None if ws is None else ws.data_ptr(), size,
                                  _mx_stream(device, stream)))
     return out
 

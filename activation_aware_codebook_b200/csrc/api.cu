@@ -759,13 +759,13 @@ aaac_status aaac_mx_linear(const aaac_mx_tensor* x, const aaac_mx_tensor* w, voi
   CHECK(take_fault());
   if (x->rows == 0) return ok();
   aaac::count_launches(1);
-  return from_cuda(aaac::launch_mx_gemm(mx_of(x), mx_of(w), Y, type == AAAC_F32, ldy, false,
-                                        (cudaStream_t)stream),
+  return from_cuda(aaac::launch_mx_gemm(mx_of(x), mx_of(w), Y, type == AAAC_F32, ldy, nullptr,
+                                        false, (cudaStream_t)stream),
                    "aaac_mx_linear");
 }
 
 size_t aaac_mx_workspace_size(int32_t fmt, int64_t rows, int64_t K, int32_t groups) {
-  if (check_mx_shape(fmt, rows, K, groups) != AAAC_OK) return 0;
+  if (check_mx_shape(fmt, rows, K, groups) != AAAC_OK || aaac::mx_own_rows(groups, rows, K)) return 0;
   return aaac::align256((size_t)rows * (size_t)(K / 2)) +
          aaac::align256(aaac::mx_scale_bytes(fmt, rows, K, groups)) +
          aaac::align256((size_t)rows * sizeof(float));
@@ -784,23 +784,32 @@ aaac_status aaac_mx_linear_ws(const aaac_mx_source* src, int64_t rows, const int
   if (!aligned4(offsets)) return fail(AAAC_ERR_ALIGN, "offsets is not 4-byte aligned");
   CHECK(check_mx_source(src, rows, w->K));
   CHECK(check_mx_out(Y, type, ldy, w->rows / w->groups, rows, 1));
-  if (rows > 0) CHECK(check_ws(ws, ws_bytes, aaac_mx_workspace_size(w->fmt, rows, w->K, w->groups)));
+  const bool own = aaac::mx_own_rows(w->groups, rows, w->K);
+  if (rows > 0 && !own)
+    CHECK(check_ws(ws, ws_bytes, aaac_mx_workspace_size(w->fmt, rows, w->K, w->groups)));
   CHECK(take_fault());
   if (rows == 0) return ok();
-  uint8_t* base = static_cast<uint8_t*>(ws);
-  aaac::MxTensor x;
+  const aaac::MxSource source = mx_source_of(src);
+  aaac::MxTensor x = {};
   x.fmt = w->fmt;
   x.groups = w->groups;
   x.rows = rows;
   x.K = w->K;
   x.offsets = offsets;
-  x.codes = base;
-  x.scales = base + aaac::align256((size_t)rows * (size_t)(w->K / 2));
+  if (own) {
+    aaac::count_launches(1);
+    return from_cuda(aaac::launch_mx_gemm(x, mx_of(w), Y, type == AAAC_F32, ldy, &source, false,
+                                          (cudaStream_t)stream),
+                     "aaac_mx_linear_ws");
+  }
+  x.codes = static_cast<uint8_t*>(ws);
+  x.scales = x.codes + aaac::align256((size_t)rows * (size_t)(w->K / 2));
   x.row_scale = reinterpret_cast<float*>(
       x.scales + aaac::align256(aaac::mx_scale_bytes(w->fmt, rows, w->K, w->groups)));
-  cudaError_t e = aaac::launch_mx_quantize(mx_source_of(src), x, (cudaStream_t)stream);
+  cudaError_t e = aaac::launch_mx_quantize(source, x, (cudaStream_t)stream);
   if (e == cudaSuccess)
-    e = aaac::launch_mx_gemm(x, mx_of(w), Y, type == AAAC_F32, ldy, true, (cudaStream_t)stream);
+    e = aaac::launch_mx_gemm(x, mx_of(w), Y, type == AAAC_F32, ldy, nullptr, true,
+                             (cudaStream_t)stream);
   if (e == cudaSuccess) aaac::count_launches(2);
   return from_cuda(e, "aaac_mx_linear_ws");
 }

@@ -168,10 +168,13 @@ size_t mx_scale_bytes(int fmt, int64_t rows, int64_t K, int groups);
 cudaError_t launch_mx_quantize(const MxSource& x, const MxTensor& q, cudaStream_t st);
 cudaError_t launch_mx_dequant(const MxTensor& q, void* out, bool f32, int64_t ldo,
                               cudaStream_t st);
+// whether the product takes these rows as they are and quantises them itself
+bool mx_own_rows(int groups, int64_t rows, int64_t K);
+// src: rows that it quantises itself (x has no codes then), or NULL;
 // overlap: the kernel before it on the stream is launch_mx_quantize's, and
 // everything but its outputs was ready before that one started
 cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f32, int64_t ldy,
-                           bool overlap, cudaStream_t st);
+                           const MxSource* src, bool overlap, cudaStream_t st);
 cudaError_t mx_timeout_flag(unsigned int* out);
 
 }  // namespace aaac

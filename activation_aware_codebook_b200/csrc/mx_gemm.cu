@@ -24,12 +24,17 @@
 // tiles; the CTAs of a cluster take a share of K each, and add their partial
 // tiles in rank order through distributed shared memory: the sum's order is
 // fixed, whatever the timing.
+// A few rows that are not quantised yet (SRC: their kind; the single tokens of
+// decoding): eight more warps quantise each stage's columns straight into its
+// shared memory, as mx_quant.cu would, while the weights stream in: one
+// launch, and no workspace.
 // Waits are bounded (tcgen05.cuh); a CTA that gives up writes NaN.
 #include <math.h>
 
 #include "common.cuh"
 #include "internal.h"
 #include "mx.cuh"
+#include "mx_run.cuh"
 #include "tcgen05.cuh"
 
 namespace aaac {
@@ -60,13 +65,26 @@ struct MxGemmArgs {
   int bf16_out;
 };
 
+// Rows to quantise on the way (SRC >= 0).
+struct RowsArgs {
+  const void* X;
+  const int32_t* index;
+  int64_t ldx;
+  int src_rows;
+  int warps;          // warps of a stage: two rows each, a power of two
+};
+constexpr int kSrcNone = -1, kSrcBf16 = 0, kSrcF32 = 1, kSrcBf16Glu = 2, kSrcF32Glu = 3;
+constexpr int kMaxOwnRows = 16;
+constexpr int kOwnWarps = 8;
+
 // How the CTAs of a launch share the work.
 constexpr int kWalk = 0;   // each walks tiles of 128 weight rows on its own
 constexpr int kSplit = 1;  // a cluster's CTAs each take a part of one tile's K
 constexpr int kPair = 2;   // two CTAs walk tiles of 256 weight rows (cta_group::2)
 
-template <int FMT, int NT, int MODE>
+template <int FMT, int NT, int MODE, int SRC>
 struct Shape {
+  static constexpr bool kOwn = SRC != kSrcNone;  // quantises its rows itself
   static constexpr bool kTwo = MODE == kPair;
   static constexpr int kTileRows = kTwo ? 2 * kWRows : kWRows;  // weight rows of a tile
   static constexpr int kSub = (NT + 127) / 128;             // 128-row scale bands a token tile meets
@@ -77,7 +95,8 @@ struct Shape {
   // 64 columns an epilogue thread at most: all of them leave tensor memory in
   // one go, so that the next tile's MMAs wait for no store
   static constexpr int kEpiWarps = NT == 256 ? 16 : 8;
-  static constexpr int kThreads = (kEpiWarp + kEpiWarps) * 32;
+  static constexpr int kOwnWarp = kEpiWarp + kEpiWarps;
+  static constexpr int kThreads = (kOwnWarp + (kOwn ? kOwnWarps : 0)) * 32;
   static constexpr int kStages = kTwo ? 5 : (NT == 256 ? 4 : (NT == 128 ? 6 : (NT == 64 ? 7 : 8)));
   static constexpr int kSmem = 1024 + kStages * kStage + (3 * kStages + 4) * 8 + 16;
   static_assert(kSmem + 4 * (kMxMaxGroups + 1) + 16 * NT + 64 <= kSmemLimit, "shared memory");
@@ -264,12 +283,12 @@ __device__ __forceinline__ void tile_at(const MxGemmArgs& a, const int* s_pre, i
   t->count = min(a.width, last - t->row);
 }
 
-template <int FMT, int NT, int MODE>
-__global__ void __launch_bounds__((Shape<FMT, NT, MODE>::kThreads), 1)
+template <int FMT, int NT, int MODE, int SRC>
+__global__ void __launch_bounds__((Shape<FMT, NT, MODE, SRC>::kThreads), 1)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                const __grid_constant__ CUtensorMap sxmap, const __grid_constant__ CUtensorMap swmap,
-               const __grid_constant__ MxGemmArgs a) {
-  using S = Shape<FMT, NT, MODE>;
+               const __grid_constant__ MxGemmArgs a, const __grid_constant__ RowsArgs own) {
+  using S = Shape<FMT, NT, MODE, SRC>;
   using TM = Tmem<NT, MODE, S::kStages>;
   constexpr bool SPLIT = MODE == kSplit, TWO = S::kTwo;
   extern __shared__ __align__(1024) unsigned char gsm[];
@@ -287,6 +306,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scale_full + S::kStages);
   __shared__ int s_pre[kMxMaxGroups + 1];  // token tiles of the groups before
   __shared__ __align__(16) float s_gx[S::kEpiWarps][FMT == kMxE4m3 && !SPLIT ? NT / (S::kEpiWarps / 4) : 4];
+  __shared__ uint32_t s_top[kMaxOwnRows];   // kOwn, E4M3: the rows' largest magnitudes,
+  __shared__ float s_scale[kMaxOwnRows];    // and their scales
   __shared__ int s_fail;
 
   // The same in every lane, and known to be: the roles of warps 0 and 1 run as
@@ -301,7 +322,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; s++) {
-      mbar_init(&full[s], 1);   // the producer's expect_tx
+      // the producer's expect_tx, and the warps that quantise
+      mbar_init(&full[s], 1 + (S::kOwn ? own.warps : 0));
       mbar_init(&empty[s], 1);  // MMA commit
       mbar_init(&scale_full[s], TWO ? 8 : 4);  // one arrive per scale warp
     }
@@ -311,6 +333,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     }
     s_fail = 0;
     s_pre[0] = 0;
+    for (int r = 0; r < kMaxOwnRows; r++) s_top[r] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -381,13 +404,15 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     const uint32_t box_bytes = (uint32_t)(a.box * kRowBytes);
     auto load_w = [&](const At& c, int st, int s) {
       if (one) {
-        mbar_arrive_expect_tx(&full[s], kWTile + c.boxes * box_bytes + S::kScale * (1 + S::kSub));
+        mbar_arrive_expect_tx(&full[s], S::kOwn ? kWTile + S::kScale
+                                                : kWTile + c.boxes * box_bytes +
+                                                      S::kScale * (1 + S::kSub));
         tma_load_2d(sW + s * kWTile, &wmap, &full[s], st * kRowBytes, c.w);
         tma_load_2d(sSW + s * S::kScale, &swmap, &full[s], st * (S::kScale / 8), c.sw);
       }
     };
     auto load_x = [&](const At& c, int st, int s) {
-      if (one) {
+      if (one && !S::kOwn) {
         for (int j = 0; j < c.boxes; j++)
           tma_load_2d(sX + s * S::kXTile + j * box_bytes, &xmap, &full[s], st * kRowBytes,
                       c.x + j * a.box);
@@ -519,6 +544,87 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       }
       if (SPLIT) break;
     }
+  } else if (S::kOwn && warp >= S::kOwnWarp) {
+    constexpr bool kF32 = SRC == kSrcF32 || SRC == kSrcF32Glu;
+    constexpr bool kGlu = SRC == kSrcBf16Glu || SRC == kSrcF32Glu;
+    const int ow = warp - S::kOwnWarp;
+    int first, last;
+    mx_group(a.rows, 0, &first, &last);
+    const int count = min(last - first, kMaxOwnRows);
+    // where the group's row r starts in X; -1: a row of zeros
+    auto row_start = [&](int r) -> int64_t {
+      if (r >= count) return -1;
+      const int src = own.index ? __ldg(own.index + first + r) : first + r;
+      return src >= 0 && src < own.src_rows ? (int64_t)src * own.ldx : -1;
+    };
+    if (FMT == kMxE4m3) {
+      const int runs = a.K >> 4;
+      for (int i0 = ow * 32; i0 < count * runs; i0 += kOwnWarps * 32) {
+        const int i = i0 + lane;
+        const int r = min(i, count * runs - 1) / runs;
+        uint32_t m = 0u;
+        if (i < count * runs) {
+          const int64_t at = row_start(r);
+          if (at >= 0) {
+            Run<kF32, kGlu> run;
+            run.load(own.X, at, (i - r * runs) * 16, a.K);
+            m = run.amax();
+          }
+        }
+        const int r0 = __shfl_sync(0xffffffffu, r, 0), r1 = __shfl_sync(0xffffffffu, r, 31);
+        if (r0 == r1) {
+          m = __reduce_max_sync(0xffffffffu, m);
+          if (lane == 0) atomicMax(&s_top[r0], m);
+        } else {
+          atomicMax(&s_top[r], m);
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kOwnWarps * 32) : "memory");
+    }
+    // this thread: one run of each of its set's stages
+    const int set = ow / own.warps, sets = kOwnWarps / own.warps;
+    const int r = (ow % own.warps) * 2 + (lane >> 4), j = lane & 15;
+    const int64_t at = row_start(r);
+    bool bad_row = false;
+    float down = 1.0f;
+    if (FMT == kMxE4m3) {
+      float g;
+      const int p = row_exponent(s_top[r], &bad_row, &g);
+      down = __uint_as_float((uint32_t)(127 - p) << 23);
+      if (j == 0) s_scale[r] = g;  // the sets write the same
+    }
+    // its place in a stage: the codes' 16-byte pieces in swizzled order, the
+    // scale byte in the tile
+    const uint32_t to = (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u +
+                        (uint32_t)((((j >> 1) ^ (r & 7)) << 4) + (j & 1) * 8);
+    const int block = FMT == kMxE8m0 ? j >> 1 : j;
+    const uint32_t scale_to = (uint32_t)((block >> 2) * kMxTileBytes + r * 16 + (block & 3));
+    Ring<S::kStages> ring;
+    bool ok = true;
+    int it = 0;
+    for (int item = item0; item < items && ok; item += step) {
+      for (int st = st_lo; st < st_hi; st++, it++, ring.next()) {
+        if (it % sets != set) continue;
+        const int col = st * kStageK + j * 16;
+        Run<kF32, kGlu> run;
+        if (at >= 0 && col < a.K) run.load(own.X, at, col, a.K);
+        else run.zero();
+        if (it >= S::kStages) ok = warp_wait(&empty[ring.s], ring.phase ^ 1);
+        if (!ok) {
+          s_fail = 1;
+          break;
+        }
+        uint32_t c[2];
+        const uint32_t byte = encode<FMT>(run, down, bad_row, c);
+        *reinterpret_cast<uint2*>(sX + ring.s * S::kXTile + to) = make_uint2(c[0], c[1]);
+        if (FMT == kMxE4m3 || (j & 1) == 0)
+          sSX[ring.s * S::kSub * S::kScale + scale_to] = (unsigned char)byte;
+        fence_proxy_async();  // generic-proxy stores -> visible to the tensor core
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[ring.s]);
+      }
+      if (SPLIT) break;
+    }
   } else {
     wait_for_x();  // the row scales
     const int q = warp & 3;                      // the TMEM lane quadrant this warp may read
@@ -538,15 +644,22 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       float gw = 1.0f;
       if (FMT == kMxE4m3 && !SPLIT) {  // fetched while the MMAs run
         if (nok) gw = __ldg(a.gw + (int64_t)t.e * a.N + n);
-        __syncwarp();
+        if (!S::kOwn) {
+          __syncwarp();
 #pragma unroll
-        for (int c = 0; c < NC; c += 32)
-          if (c + lane < NC)
-            gx[c + lane] = c + lane < mine ? __ldg(a.gx + t.row + part * NC + c + lane) : 0.0f;
-        __syncwarp();
+          for (int c = 0; c < NC; c += 32)
+            if (c + lane < NC)
+              gx[c + lane] = c + lane < mine ? __ldg(a.gx + t.row + part * NC + c + lane) : 0.0f;
+          __syncwarp();
+        }
       }
       const bool got = __all_sync(0xffffffffu, mbar_wait(&acc_full[b], (i / TM::kBufs) & 1));
       tc_fence_after();
+      if (FMT == kMxE4m3 && !SPLIT && S::kOwn) {  // written before the last stage was
+        __syncwarp();
+        if (lane < NC) gx[lane] = lane < mine ? s_scale[part * NC + lane] : 0.0f;
+        __syncwarp();
+      }
       const bool fail = !got || s_fail;
       const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NT + part * NC);
       if (SPLIT) {
@@ -680,7 +793,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
             v[3] = __fadd_rn(v[3], part[k].w);
           }
         if (FMT == kMxE4m3) {
-          const float g = __ldg(a.gx + t.row + c);
+          const float g = S::kOwn ? s_scale[c] : __ldg(a.gx + t.row + c);
           const float* gw = a.gw + (int64_t)t.e * a.N;
 #pragma unroll
           for (int j = 0; j < 4; j++)
@@ -739,26 +852,20 @@ struct Maps {
 // Codes as bytes, 128 of a row at a time.  Scale tiles as 8-byte units, a
 // stage's tiles along K at a time (tiles past K read as zero) and as many
 // bands as a token tile has.
-cudaError_t make_maps(const MxTensor& x, const MxTensor& w, const MxPlan& p, int box, Maps* m) {
-  EncodeTiledFn enc = nullptr;
-  cudaError_t e = encode_fn(&enc);
-  const int64_t scale_row = mx_tiles_k(x.fmt, x.K) * kMxTileBytes;
-  const int units = (x.fmt == kMxE8m0 ? 2 : 4) * kMxTileBytes / 8;
-  if (e == cudaSuccess) e = byte_map(enc, &m->x, x.codes, x.K / 2, x.rows, 1, kRowBytes, box);
-  if (e == cudaSuccess) e = byte_map(enc, &m->w, w.codes, w.K / 2, w.rows, 1, kRowBytes, kWRows);
-  if (e == cudaSuccess)
-    e = byte_map(enc, &m->sx, x.scales, scale_row, mx_bands(x.rows, x.groups), 8, units,
-                 (p.nt + 127) / 128);
-  if (e == cudaSuccess)
-    e = byte_map(enc, &m->sw, w.scales, scale_row, mx_bands(w.rows, w.groups), 8, units, 1);
-  return e;
+cudaError_t make_maps(EncodeTiledFn enc, const MxTensor& t, int box_rows, int box_bands,
+                      CUtensorMap* codes, CUtensorMap* scales) {
+  const int units = (t.fmt == kMxE8m0 ? 2 : 4) * kMxTileBytes / 8;
+  const cudaError_t e = byte_map(enc, codes, t.codes, t.K / 2, t.rows, 1, kRowBytes, box_rows);
+  if (e != cudaSuccess) return e;
+  return byte_map(enc, scales, t.scales, mx_tiles_k(t.fmt, t.K) * kMxTileBytes,
+                  mx_bands(t.rows, t.groups), 8, units, box_bands);
 }
 
-template <int FMT, int NT, int MODE>
+template <int FMT, int NT, int MODE, int SRC = kSrcNone>
 cudaError_t launch_t(const Maps& m, const MxGemmArgs& a, const MxPlan& p, bool overlap,
-                     cudaStream_t st) {
-  using S = Shape<FMT, NT, MODE>;
-  cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<FMT, NT, MODE>,
+                     cudaStream_t st, const RowsArgs& own = RowsArgs{}) {
+  using S = Shape<FMT, NT, MODE, SRC>;
+  cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<FMT, NT, MODE, SRC>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -783,7 +890,7 @@ cudaError_t launch_t(const Maps& m, const MxGemmArgs& a, const MxPlan& p, bool o
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NT, MODE>, m.x, m.w, m.sx, m.sw, a);
+  return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NT, MODE, SRC>, m.x, m.w, m.sx, m.sw, a, own);
 }
 
 template <int FMT, int MODE>
@@ -795,6 +902,23 @@ cudaError_t launch_m(const Maps& m, const MxGemmArgs& a, const MxPlan& p, bool o
     case 128: return launch_t<FMT, 128, MODE>(m, a, p, overlap, st);
     default: return launch_t<FMT, 256, MODE>(m, a, p, overlap, st);
   }
+}
+
+template <int FMT, int SRC>
+cudaError_t launch_own(const Maps& m, const MxGemmArgs& a, const MxPlan& p, const RowsArgs& own,
+                       cudaStream_t st) {
+  return p.split > 1 ? launch_t<FMT, 32, kSplit, SRC>(m, a, p, false, st, own)
+                     : launch_t<FMT, 32, kWalk, SRC>(m, a, p, false, st, own);
+}
+
+template <int FMT>
+cudaError_t launch_own_f(const Maps& m, const MxGemmArgs& a, const MxPlan& p, const MxSource& x,
+                         const RowsArgs& own, cudaStream_t st) {
+  if (x.f32)
+    return x.swiglu ? launch_own<FMT, kSrcF32Glu>(m, a, p, own, st)
+                    : launch_own<FMT, kSrcF32>(m, a, p, own, st);
+  return x.swiglu ? launch_own<FMT, kSrcBf16Glu>(m, a, p, own, st)
+                  : launch_own<FMT, kSrcBf16>(m, a, p, own, st);
 }
 
 template <int FMT>
@@ -865,19 +989,37 @@ MxPlan mx_plan(int groups, int64_t rows, int64_t N, int64_t K) {
   return p;
 }
 
+// Few rows, and short: every CTA quantises its part of them itself (and reads
+// all of them for the rows' maxima).
+bool mx_own_rows(int groups, int64_t rows, int64_t K) {
+  return groups == 1 && rows <= kMaxOwnRows && rows * K <= 32768;
+}
+
 cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f32, int64_t ldy,
-                           bool overlap, cudaStream_t st) {
+                           const MxSource* src, bool overlap, cudaStream_t st) {
+  EncodeTiledFn enc = nullptr;
+  cudaError_t e = encode_fn(&enc);
+  if (e != cudaSuccess) return e;
   const int64_t N = w.rows / w.groups;
   const MxPlan p = mx_plan(x.groups, x.rows, N, x.K);
   // One copy for all of a tile's token rows; ragged groups leave many tiles
   // part empty and take pieces, of which only those with rows are fetched.
   const int box = x.groups == 1 ? (p.pair ? p.width / 2 : p.width) : (p.nt < 128 ? 32 : 64);
-  Maps m;
-  const cudaError_t e = make_maps(x, w, p, box, &m);
+  Maps m = {};
+  e = make_maps(enc, w, kWRows, 1, &m.w, &m.sw);
+  if (e == cudaSuccess && !src) e = make_maps(enc, x, box, (p.nt + 127) / 128, &m.x, &m.sx);
   if (e != cudaSuccess) return e;
   const MxGemmArgs a{x.row_scale, w.row_scale, Y, ldy,
                      MxRows{x.offsets, x.groups, (int)x.rows}, (int)N, (int)x.K,
-                     (int)((N + kWRows - 1) / kWRows + p.pair) / (1 + p.pair), p.stages, p.width, box, f32 ? 0 : 1};
+                     (int)((N + kWRows - 1) / kWRows + p.pair) / (1 + p.pair), p.stages, p.width, box,
+                     f32 ? 0 : 1};
+  if (src) {
+    int warps = 1;
+    while (2 * warps < (int)x.rows) warps *= 2;
+    const RowsArgs own{src->X, src->index, src->ldx, (int)src->rows, warps};
+    return x.fmt == kMxE8m0 ? launch_own_f<kMxE8m0>(m, a, p, *src, own, st)
+                            : launch_own_f<kMxE4m3>(m, a, p, *src, own, st);
+  }
   return x.fmt == kMxE8m0 ? launch_f<kMxE8m0>(m, a, p, overlap, st)
                           : launch_f<kMxE4m3>(m, a, p, overlap, st);
 }

@@ -20,7 +20,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "mx.cuh"
-#include "tcgen05.cuh"
+#include "mx_run.cuh"
 
 namespace aaac {
 
@@ -91,210 +91,20 @@ __device__ __forceinline__ int64_t scale_ragged(const MxRows& g, int r, int lane
   return scale_place((uint32_t)e, (uint32_t)min(first, r), (uint32_t)r, tiles_k);
 }
 
-__device__ __forceinline__ float rcp_approx(float d) {  // within a step of 1 / d
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-  return r;
-}
-
-// x / d from r, a reciprocal of d: the quotient x r is off by steps, its
-// residual is exact in an fma, and adding the residual's quotient rounds to
-// the nearest (Markstein, "Computation of elementary functions on the IBM
-// RISC System/6000 processor", 1990; always so with r rounded to nearest, and
-// all but about one time in a million with r a step off).  Three instructions
-// where a division per value takes about ten.
-__device__ __forceinline__ float div_by(float x, float d, float r) {
-  const float q = __fmul_rn(x, r);
-  return __fmaf_rn(-r, __fmaf_rn(d, q, -x), q);  // these signs keep a zero's
-}
-
-// silu(a) b, each step in fp32.  exp(-a) is held below 2^126, so that its
-// reciprocal is a normal number: silu(a) is below 1e-35 there.
-__device__ __forceinline__ float silu_mul(float a, float b) {
-  const float d = __fadd_rn(1.0f, expf(fminf(-a, 87.0f)));
-  return __fmul_rn(div_by(a, d, rcp_approx(d)), b);
-}
-
-// 16 values of a row.  bf16 stays packed: half the registers.
-template <bool F32, bool SWIGLU>
-struct Run {
-  float v[16];
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < 16; i++) v[i] = 0.0f;
-  }
-  __device__ __forceinline__ static void load16(const void* X, int64_t at, float (&o)[16]) {
-    if (F32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(X) + at);
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float4 q = __ldg(p + i);
-        o[4 * i] = q.x;
-        o[4 * i + 1] = q.y;
-        o[4 * i + 2] = q.z;
-        o[4 * i + 3] = q.w;
-      }
-    } else {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(X) + at);
-#pragma unroll
-      for (int i = 0; i < 2; i++) {
-        const uint4 q = __ldg(p + i);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          o[8 * i + 2 * j] = bf16_lo(w[j]);
-          o[8 * i + 2 * j + 1] = bf16_hi(w[j]);
-        }
-      }
-    }
-  }
-  // row_at: the source row's first element; col: this run's first column
-  __device__ __forceinline__ void load(const void* X, int64_t row_at, int col, int K) {
-    load16(X, row_at + col, v);
-    if (SWIGLU) {
-      float u[16];
-      load16(X, row_at + K + col, u);
-#pragma unroll
-      for (int i = 0; i < 16; i++) v[i] = silu_mul(v[i], u[i]);
-    }
-  }
-  // the largest magnitude's bits (a NaN or infinity is above every number)
-  __device__ __forceinline__ uint32_t amax() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-      float t;
-      asm("max.NaN.f32 %0, %1, %2;" : "=f"(t) : "f"(__uint_as_float(m)), "f"(fabsf(v[i])));
-      m = __float_as_uint(t);
-    }
-    return m;
-  }
-  // half h's values times a power of two
-  __device__ __forceinline__ void scaled(int h, float f, float (&o)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; i++) o[i] = __fmul_rn(v[8 * h + i], f);
-  }
-};
-
-template <>
-struct Run<false, false> {
-  uint32_t w[8];
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < 8; i++) w[i] = 0u;
-  }
-  __device__ __forceinline__ void load(const void* X, int64_t row_at, int col, int) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(X) + row_at + col);
-    const uint4 a = __ldg(p), b = __ldg(p + 1);
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-  }
-  __device__ __forceinline__ uint32_t amax() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; i++) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-    return max(m << 16, m & 0xffff0000u);
-  }
-  // The product is exact in bf16 too (below 2^-126, where it is not, the code
-  // is 0 either way): one multiply for two values.
-  __device__ __forceinline__ void scaled(int h, float f, float (&o)[8]) const {
-    const uint32_t f2 = __float_as_uint(f) | __float_as_uint(f) >> 16;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      uint32_t p;
-      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p) : "r"(w[4 * h + i]), "r"(f2));
-      o[2 * i] = bf16_lo(p);
-      o[2 * i + 1] = bf16_hi(p);
-    }
-  }
-};
-
-// An E4M3 byte without its sign (a scale), exact in fp32.
-__device__ __forceinline__ float e4m3_value(uint32_t byte) {
-  float f;
-  asm("{\n .reg .b16 b, l, h;\n .reg .b32 p;\n cvt.u16.u32 b, %1;\n"
-      " cvt.rn.f16x2.e4m3x2 p, b;\n mov.b32 {l, h}, p;\n cvt.f32.f16 %0, l;\n}\n"
-      : "=f"(f)
-      : "r"(byte & 0x7fu));
-  return f;
-}
-
-// Eight E2M1 codes of eight floats, the first in the lowest nibble; round to
-// nearest even, magnitudes above 6 to 6.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&q)[8]) {
-  uint32_t r;
-  asm("{\n .reg .b8 b0, b1, b2, b3;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
-      " mov.b32 %0, {b0, b1, b2, b3};\n}\n"
-      : "=r"(r)
-      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
-  return r;
-}
-
-constexpr uint32_t kInfBits = 0x7f800000u;
-
 // Codes and scale of one run, written out.  Every lane of the warp takes part
 // (the lanes of a scale word meet in shuffles); `in` says whether this lane's
 // run lies inside the row.  down: E4M3 only, 2^-p.
 template <int FMT, bool F32, bool SWIGLU>
 __device__ __forceinline__ void emit(const Run<F32, SWIGLU>& run, bool in, int col, int lane,
                                      float down, bool bad_row, uint8_t* crow, uint8_t* srow) {
-  const uint32_t own = run.amax();
-  uint32_t word, c[2];
-  if (FMT == kMxE8m0) {
-    const uint32_t m = max(own, __shfl_xor_sync(0xffffffffu, own, 1));
-    const bool bad = m >= kInfBits;
-    const uint32_t byte = bad ? 255u : (uint32_t)max((int)(m >> 23) - 2, 0);
-    // byte <= 252 for finite values, so 2^(127 - byte) is a normal number
-    const float inv = __uint_as_float((254u - byte) << 23);
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      float q[8];
-      run.scaled(h, inv, q);
-      c[h] = bad ? 0u : e2m1x8(q);
-    }
-    word = in ? byte << (8 * ((lane >> 1) & 3)) : 0u;
-    word |= __shfl_xor_sync(0xffffffffu, word, 2);
-    word |= __shfl_xor_sync(0xffffffffu, word, 4);
-  } else {
-    const float top = __fmul_rn(__uint_as_float(own), down);
-    const uint32_t byte = bad_row ? 0u
-                                  : (uint32_t)__nv_cvt_float_to_fp8(
-                                        div_by(top, 6.0f, 1.0f / 6.0f), __NV_SATFINITE, __NV_E4M3);
-    const float s = e4m3_value(byte);
-    // The quotient x' / s, x' = x * 2^-p.
-    // bf16: with r a little below 1/s and rl = fp32_RN(r (1 - s r)) > 0, the
-    // rest of 1/s, fma(x', r, x' rl) is the quotient to within 2^-24 (1 +
-    // 2^-19) of it, and exactly the quotient where that is a number of few
-    // bits (and keeps a zero's sign).  A border between codes is such a
-    // number, and a quotient of an 8-bit x' and a 4-bit s that is not on a
-    // border is 2^-9 or more away from it; so every code is the one that the
-    // exact quotient has.
-    // fp32 values have no such gap and take the correctly rounded quotient
-    // (its residual can only underflow where the code is 0 anyway).
-    float r = rcp_approx(s);
-    if (F32 || SWIGLU) r = __fmaf_rn(__fmaf_rn(-s, r, 1.0f), r, r);
-    else r = __fmul_rn(r, 1.0f - 0x1p-22f);
-    const float rl = __fmul_rn(__fmaf_rn(-s, r, 1.0f), r);
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      float q[8];
-      run.scaled(h, down, q);
-#pragma unroll
-      for (int i = 0; i < 8; i++)
-        q[i] = (F32 || SWIGLU) ? div_by(q[i], s, r) : __fmaf_rn(q[i], r, __fmul_rn(q[i], rl));
-      c[h] = byte == 0u ? 0u : e2m1x8(q);
-    }
-    word = in ? byte << (8 * (lane & 3)) : 0u;
-    word |= __shfl_xor_sync(0xffffffffu, word, 1);
-    word |= __shfl_xor_sync(0xffffffffu, word, 2);
-  }
+  uint32_t c[2];
+  const uint32_t byte = encode<FMT>(run, down, bad_row, c);
+  constexpr int kLanes = FMT == kMxE8m0 ? 8 : 4;  // lanes of one scale word
+  uint32_t word = in ? byte << (8 * (lane % kLanes * 4 / kLanes)) : 0u;
+  word |= __shfl_xor_sync(0xffffffffu, word, kLanes / 4);
+  word |= __shfl_xor_sync(0xffffffffu, word, kLanes / 2);
   if (in) {
     *reinterpret_cast<uint2*>(crow + (col >> 1)) = make_uint2(c[0], c[1]);
-    constexpr int kLanes = FMT == kMxE8m0 ? 8 : 4;  // lanes of one scale word
     if (lane % kLanes == 0)
       *reinterpret_cast<uint32_t*>(srow + (int64_t)(col / (16 * kLanes)) * kMxTileBytes) = word;
   }
@@ -346,12 +156,10 @@ quantize_kernel(const __grid_constant__ QuantArgs a) {
       __syncthreads();
       m = __reduce_max_sync(0xffffffffu, lane < (T >> 5) ? s_max[lane] : 0u);
     }
-    bad_row = m >= kInfBits;
-    int p = max((int)(m >> 23) - 138 + ((m & 0x7fffffu) > 0x280000u ? 1 : 0), -126);
-    if (m == 0u || bad_row) p = 0;
+    float g;
+    const int p = row_exponent(m, &bad_row, &g);
     down = __uint_as_float((uint32_t)(127 - p) << 23);
-    if (threadIdx.x == 0)
-      a.row_scale[row] = __uint_as_float(bad_row ? 0x7fc00000u : (uint32_t)(127 + p) << 23);
+    if (threadIdx.x == 0) a.row_scale[row] = g;
   }
   uint8_t* crow = a.codes + (int64_t)row * (a.K >> 1);
   uint8_t* srow = a.scales + at;

@@ -347,6 +347,84 @@ def test_group_rows_do_not_depend_on_their_batch(fmt):
     assert torch.equal(Z, Y[perm.cuda()])
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("rows,K,N", [(1, 32, 130), (1, 4096, 300), (2, 2080, 70), (3, 544, 128),
+                                      (5, 1056, 200), (9, 288, 129), (16, 2048, 260),
+                                      (4, 96, 128 * 151), (1, 32768, 128), (7, 2304, 128 * 150)])
+def test_few_rows_are_quantised_by_the_product(fmt, dtype, swiglu, rows, K, N):
+    """Up to 16 rows need no workspace: the same bits as quantisation and
+    product, for K split over CTAs, whole, and for CTAs with several tiles;
+    rows picked by an index with padding."""
+    assert bb.mx_workspace_size(fmt, rows, K, 1) == 0
+    x = activations(rows + 2, (2 if swiglu else 1) * K, rows + K, dtype).cuda()
+    W = bb.mx_quantize(synth.make_weight(N, K, 3).cuda(), fmt)
+    index = torch.arange(rows, dtype=torch.int32).flip(0)
+    if rows > 1:
+        index[rows // 2] = -1
+    for rows_arg in (None, index.cuda()):
+        src = x[:rows] if rows_arg is None else x
+        X = bb.mx_quantize(src, fmt, rows=rows_arg, swiglu=swiglu)
+        for out_dtype in (torch.float32, torch.bfloat16):
+            Y = bb.mx_linear(X, W, out_dtype=out_dtype)
+            Z = bb.mx_linear(src, W, rows=rows_arg, swiglu=swiglu, out_dtype=out_dtype)
+            assert torch.equal(Y, Z)
+    torch.cuda.synchronize()
+    check_product(Y, X, W, [0, rows], 1)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_few_rows_of_one_ragged_group(fmt):
+    """Rows outside the one group are left as they were; a NaN stays in its row."""
+    K, N, R = 608, 200, 12
+    x = activations(R, K, 5)
+    x[6, 100] = float("nan")
+    W = bb.mx_quantize(synth.make_weight(N, K, 3).cuda(), fmt)
+    for lo, hi in ((0, 12), (3, 9), (5, 5), (11, 12)):
+        off = torch.tensor([lo, hi], dtype=torch.int32).cuda()
+        Y = torch.full((R, N), 2.5, device="cuda")
+        bb.mx_linear(x.cuda(), W, out=Y, offsets=off)
+        X = bb.mx_quantize(x.cuda(), fmt, offsets=off)
+        Z = torch.full((R, N), 2.5, device="cuda")
+        bb.mx_linear(X, W, out=Z)
+        assert torch.equal(Y.nan_to_num(7.0), Z.nan_to_num(7.0))
+        assert torch.isnan(Y).any(1).cpu().tolist() == [lo <= r < hi and r == 6 for r in range(R)]
+        assert (Y[:lo] == 2.5).all() and (Y[hi:] == 2.5).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(160, 128 * 80, 288), (1100, 5100, 544), (2300, 2600, 320)])
+def test_linear_wide_tiles(fmt, M, N, K):
+    """Tiles of 192 and 256 tokens, by single CTAs and by pairs, with last tiles
+    of few rows and weight rows that end inside a tile."""
+    X = bb.mx_quantize(activations(M, K, M).cuda(), fmt)
+    W = bb.mx_quantize(synth.make_weight(N, K, N).cuda(), fmt)
+    for dtype in (torch.float32, torch.bfloat16):
+        Y = bb.mx_linear(X, W, out_dtype=dtype)
+        torch.cuda.synchronize()
+        check_product(Y, X, W, [0, M], 1)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_linear_grouped_wide_tiles(fmt):
+    """Ragged groups large enough for pairs of CTAs: tiles that start at any row."""
+    offsets = [5, 5, 700, 701, 1500, 1900, 2611]
+    E, N, K = 6, 2600, 352
+    x = activations(2620, K, 4).cuda()
+    off = torch.tensor(offsets, dtype=torch.int32).cuda()
+    X = bb.mx_quantize(x, fmt, groups=E, offsets=off)
+    W = bb.mx_quantize(synth.make_weight(E * N, K, E).cuda(), fmt, groups=E)
+    assert bb.mx_launch_plan(E, 2620, N, K)["rows"] == 256
+    Y = torch.full((2620, N), 3.0, device="cuda")
+    bb.mx_linear(X, W, out=Y)
+    torch.cuda.synchronize()
+    check_product(Y, X, W, offsets, E, y0=3.0)
+    Z = torch.full((2620, N), 3.0, device="cuda")
+    bb.mx_linear(x, W, out=Z, offsets=off)
+    assert torch.equal(Y, Z)
+
+
 def test_empty_calls():
     for fmt in FMTS:
         W = bb.mx_quantize(synth.make_weight(40, 64, 1).cuda(), fmt)
