@@ -59,4 +59,17 @@ __host__ __device__ inline int64_t mx_bands(int64_t rows, int groups) {
   return rows / kMxTileRows + groups;
 }
 
+// Kernels of the microscaled calls are launched so that they may start while
+// the kernel before them on the stream still runs (programmatic dependent
+// launch), set themselves up, and then wait for all that came before.  A kernel
+// touches no global memory before after_previous(), but for one case: the
+// product behind its own quantisation reads weights and offsets earlier, which
+// is sound because the quantisation lets it start only after its own wait.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 }  // namespace aaac

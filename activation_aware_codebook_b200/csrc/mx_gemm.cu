@@ -63,6 +63,7 @@ struct MxGemmArgs {
   int width;          // tokens of a tile: NT, or fewer
   int box;            // token rows of one TMA copy
   int bf16_out;
+  int ahead;          // all but X was ready before the kernel before this one
 };
 
 // Rows to quantise on the way (SRC >= 0).
@@ -195,11 +196,6 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
           : "memory");
 }
 
-// What a kernel launched to overlap the quantisation before it must not read
-// early: the quantised X and its row scales.  Returns at once otherwise.
-__device__ __forceinline__ void wait_for_x() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
 
 __device__ __forceinline__ float4 ld_cluster_f4(const float* local, uint32_t rank) {
   uint32_t at;
@@ -315,11 +311,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   // are worked out in uniform registers, where TMA and MMA want them.
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < a.rows.groups; e += S::kThreads) {
-    int first, last;
-    mx_group(a.rows, e, &first, &last);
-    s_pre[e + 1] = (last - first + a.width - 1) / a.width;
-  }
+  let_next_start();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; s++) {
       // the producer's expect_tx, and the warps that quantise
@@ -349,6 +341,12 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
   }
+  if (!a.ahead) after_previous();
+  for (int e = threadIdx.x; e < a.rows.groups; e += S::kThreads) {
+    int first, last;
+    mx_group(a.rows, e, &first, &last);
+    s_pre[e + 1] = (last - first + a.width - 1) / a.width;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -364,7 +362,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       sum += __shfl_sync(0xffffffffu, v, 31);
     }
   }
-  __syncthreads();
+  if (a.rows.groups > 1) __syncthreads();
   const uint32_t tmem = *tmem_slot;
 
   // this CTA's tiles and its share of K
@@ -428,7 +426,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       const At c = at_of(t);
       for (; ahead < min(nst, S::kStages); ahead++) load_w(c, st_lo + ahead, ahead);
     }
-    wait_for_x();
+    after_previous();  // X's codes and scales
     int it = 0;
     bool ok = true;
     Ring<S::kStages> ring;
@@ -626,7 +624,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       if (SPLIT) break;
     }
   } else {
-    wait_for_x();  // the row scales
+    after_previous();  // the row scales
     const int q = warp & 3;                      // the TMEM lane quadrant this warp may read
     const int part = (warp - kEpiWarp) >> 2;     // its share of the token columns
     constexpr int NC = NT / (S::kEpiWarps / 4);
@@ -862,7 +860,7 @@ cudaError_t make_maps(EncodeTiledFn enc, const MxTensor& t, int box_rows, int bo
 }
 
 template <int FMT, int NT, int MODE, int SRC = kSrcNone>
-cudaError_t launch_t(const Maps& m, const MxGemmArgs& a, const MxPlan& p, bool overlap,
+cudaError_t launch_t(const Maps& m, const MxGemmArgs& a, const MxPlan& p,
                      cudaStream_t st, const RowsArgs& own = RowsArgs{}) {
   using S = Shape<FMT, NT, MODE, SRC>;
   cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<FMT, NT, MODE, SRC>,
@@ -883,32 +881,30 @@ cudaError_t launch_t(const Maps& m, const MxGemmArgs& a, const MxPlan& p, bool o
     attr[n].val.clusterDim.z = 1;
     n++;
   }
-  if (overlap) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    n++;
-  }
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n].val.programmaticStreamSerializationAllowed = 1;
+  n++;
   cfg.attrs = attr;
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NT, MODE, SRC>, m.x, m.w, m.sx, m.sw, a, own);
 }
 
 template <int FMT, int MODE>
-cudaError_t launch_m(const Maps& m, const MxGemmArgs& a, const MxPlan& p, bool overlap,
+cudaError_t launch_m(const Maps& m, const MxGemmArgs& a, const MxPlan& p,
                      cudaStream_t st) {
   switch (p.nt) {
-    case 32: return launch_t<FMT, 32, MODE>(m, a, p, overlap, st);
-    case 64: return launch_t<FMT, 64, MODE>(m, a, p, overlap, st);
-    case 128: return launch_t<FMT, 128, MODE>(m, a, p, overlap, st);
-    default: return launch_t<FMT, 256, MODE>(m, a, p, overlap, st);
+    case 32: return launch_t<FMT, 32, MODE>(m, a, p, st);
+    case 64: return launch_t<FMT, 64, MODE>(m, a, p, st);
+    case 128: return launch_t<FMT, 128, MODE>(m, a, p, st);
+    default: return launch_t<FMT, 256, MODE>(m, a, p, st);
   }
 }
 
 template <int FMT, int SRC>
 cudaError_t launch_own(const Maps& m, const MxGemmArgs& a, const MxPlan& p, const RowsArgs& own,
                        cudaStream_t st) {
-  return p.split > 1 ? launch_t<FMT, 32, kSplit, SRC>(m, a, p, false, st, own)
-                     : launch_t<FMT, 32, kWalk, SRC>(m, a, p, false, st, own);
+  return p.split > 1 ? launch_t<FMT, 32, kSplit, SRC>(m, a, p, st, own)
+                     : launch_t<FMT, 32, kWalk, SRC>(m, a, p, st, own);
 }
 
 template <int FMT>
@@ -922,11 +918,11 @@ cudaError_t launch_own_f(const Maps& m, const MxGemmArgs& a, const MxPlan& p, co
 }
 
 template <int FMT>
-cudaError_t launch_f(const Maps& m, const MxGemmArgs& a, const MxPlan& p, bool overlap,
+cudaError_t launch_f(const Maps& m, const MxGemmArgs& a, const MxPlan& p,
                      cudaStream_t st) {
-  if (p.pair) return launch_t<FMT, 256, kPair>(m, a, p, overlap, st);
-  return p.split > 1 ? launch_m<FMT, kSplit>(m, a, p, overlap, st)
-                     : launch_m<FMT, kWalk>(m, a, p, overlap, st);
+  if (p.pair) return launch_t<FMT, 256, kPair>(m, a, p, st);
+  return p.split > 1 ? launch_m<FMT, kSplit>(m, a, p, st)
+                     : launch_m<FMT, kWalk>(m, a, p, st);
 }
 
 }  // namespace
@@ -1012,7 +1008,7 @@ cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f
   const MxGemmArgs a{x.row_scale, w.row_scale, Y, ldy,
                      MxRows{x.offsets, x.groups, (int)x.rows}, (int)N, (int)x.K,
                      (int)((N + kWRows - 1) / kWRows + p.pair) / (1 + p.pair), p.stages, p.width, box,
-                     f32 ? 0 : 1};
+                     f32 ? 0 : 1, overlap ? 1 : 0};
   if (src) {
     int warps = 1;
     while (2 * warps < (int)x.rows) warps *= 2;
@@ -1020,8 +1016,8 @@ cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f
     return x.fmt == kMxE8m0 ? launch_own_f<kMxE8m0>(m, a, p, *src, own, st)
                             : launch_own_f<kMxE4m3>(m, a, p, *src, own, st);
   }
-  return x.fmt == kMxE8m0 ? launch_f<kMxE8m0>(m, a, p, overlap, st)
-                          : launch_f<kMxE4m3>(m, a, p, overlap, st);
+  return x.fmt == kMxE8m0 ? launch_f<kMxE8m0>(m, a, p, st)
+                          : launch_f<kMxE4m3>(m, a, p, st);
 }
 
 cudaError_t mx_timeout_flag(unsigned int* out) {

@@ -116,8 +116,8 @@ template <int FMT, bool F32, bool SWIGLU, int C>
 __global__ void __launch_bounds__(1024)
 quantize_kernel(const __grid_constant__ QuantArgs a) {
   __shared__ uint32_t s_max[32];
-  // the product that follows may set itself up while this kernel runs
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_previous();
+  let_next_start();
   const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int T = blockDim.x;
   const int src = a.index ? __ldg(a.index + row) : row;
@@ -180,21 +180,37 @@ quantize_kernel(const __grid_constant__ QuantArgs a) {
   }
 }
 
+// A launch that may start while the kernel before it runs (see mx.cuh).
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t st,
+                   const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Runs a thread holds.  With many rows: enough that a block's loads cover the
 // time its predecessor on the SM takes to compute and leave (8192 x 14336 to
 // E8M0: 78 us at one run a thread).  With few rows: one, for the most threads.
 template <int FMT, bool F32, bool SWIGLU>
-void launch_quantize_t(const QuantArgs& a, cudaStream_t st) {
+cudaError_t launch_quantize_t(const QuantArgs& a, cudaStream_t st) {
   constexpr int kMany = F32 || SWIGLU ? 2 : 4;
   const int runs = a.K >> 4;
   auto threads = [](int n) { return n < 1024 ? (n + 31) / 32 * 32 : 1024; };
   const unsigned grid = (unsigned)a.rows.rows;
   if (runs > 1024 * kMany)
-    quantize_kernel<FMT, F32, SWIGLU, 0><<<grid, 1024, 0, st>>>(a);
-  else if (runs > 1024 || (!SWIGLU && a.rows.rows >= 4 * 148))
-    quantize_kernel<FMT, F32, SWIGLU, kMany><<<grid, threads((runs + kMany - 1) / kMany), 0, st>>>(a);
-  else
-    quantize_kernel<FMT, F32, SWIGLU, 1><<<grid, threads(runs), 0, st>>>(a);
+    return launch(quantize_kernel<FMT, F32, SWIGLU, 0>, grid, 1024, st, a);
+  if (runs > 1024 || (!SWIGLU && a.rows.rows >= 4 * 148))
+    return launch(quantize_kernel<FMT, F32, SWIGLU, kMany>, grid,
+                  threads((runs + kMany - 1) / kMany), st, a);
+  return launch(quantize_kernel<FMT, F32, SWIGLU, 1>, grid, threads(runs), st, a);
 }
 
 // 16 values from two words of codes: E2M1 * s, exact in fp32.
@@ -286,6 +302,8 @@ template <int FMT, bool F32>
 __global__ void __launch_bounds__(kDeqThreads)
 mx_dequant_kernel(const __grid_constant__ DequantArgs a, int row0, uint32_t total, Div runs,
                   Div per) {
+  after_previous();
+  let_next_start();
   const uint32_t i0 = blockIdx.x * (kDeqThreads * kDeqRuns) + threadIdx.x;
   uint2 w[kDeqRuns];
   uint32_t sb[kDeqRuns];
@@ -315,6 +333,8 @@ mx_dequant_kernel(const __grid_constant__ DequantArgs a, int row0, uint32_t tota
 template <int FMT, bool F32>
 __global__ void __launch_bounds__(kDeqThreads)
 mx_dequant_ragged_kernel(const __grid_constant__ DequantArgs a) {
+  after_previous();
+  let_next_start();
   const int row = blockIdx.x;
   const int64_t at = scale_ragged(a.rows, row, threadIdx.x & 31, a.tiles_k);
   if (at < 0) return;
@@ -330,23 +350,23 @@ mx_dequant_ragged_kernel(const __grid_constant__ DequantArgs a) {
 }
 
 template <int FMT, bool F32>
-void launch_dequant_t(const DequantArgs& a, cudaStream_t st) {
+cudaError_t launch_dequant_t(const DequantArgs& a, cudaStream_t st) {
   const int runs = a.K >> 4;
-  if (a.rows.offsets) {
-    mx_dequant_ragged_kernel<FMT, F32><<<(unsigned)a.rows.rows,
-                                         runs < kDeqThreads ? (runs + 31) / 32 * 32 : kDeqThreads, 0,
-                                         st>>>(a);
-    return;
-  }
+  if (a.rows.offsets)
+    return launch(mx_dequant_ragged_kernel<FMT, F32>, (unsigned)a.rows.rows,
+                  runs < kDeqThreads ? (runs + 31) / 32 * 32 : kDeqThreads, st, a);
   // as many rows to a launch as 2^30 runs hold
   const int64_t step = ((int64_t)1 << 30) / runs;
   for (int64_t r0 = 0; r0 < a.rows.rows; r0 += step) {
     const int64_t n = a.rows.rows - r0 < step ? a.rows.rows - r0 : step;
     const uint32_t total = (uint32_t)(n * runs);
     const unsigned grid = (total + kDeqThreads * kDeqRuns - 1) / (kDeqThreads * kDeqRuns);
-    mx_dequant_kernel<FMT, F32><<<grid, kDeqThreads, 0, st>>>(
-        a, (int)r0, total, Div((uint32_t)runs), Div((uint32_t)(a.rows.rows / a.rows.groups)));
+    const cudaError_t e =
+        launch(mx_dequant_kernel<FMT, F32>, grid, kDeqThreads, st, a, (int)r0, total,
+               Div((uint32_t)runs), Div((uint32_t)(a.rows.rows / a.rows.groups)));
+    if (e != cudaSuccess) return e;
   }
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -360,23 +380,17 @@ cudaError_t launch_mx_quantize(const MxSource& x, const MxTensor& q, cudaStream_
               MxRows{q.offsets, q.groups, (int)q.rows}, q.codes, q.scales, q.row_scale,
               mx_tiles_k(q.fmt, q.K), Div((uint32_t)(q.rows / q.groups ? q.rows / q.groups : 1))};
   if (q.fmt == kMxE8m0) {
-    if (x.f32) {
-      if (x.swiglu) launch_quantize_t<kMxE8m0, true, true>(a, st);
-      else launch_quantize_t<kMxE8m0, true, false>(a, st);
-    } else {
-      if (x.swiglu) launch_quantize_t<kMxE8m0, false, true>(a, st);
-      else launch_quantize_t<kMxE8m0, false, false>(a, st);
-    }
-  } else {
-    if (x.f32) {
-      if (x.swiglu) launch_quantize_t<kMxE4m3, true, true>(a, st);
-      else launch_quantize_t<kMxE4m3, true, false>(a, st);
-    } else {
-      if (x.swiglu) launch_quantize_t<kMxE4m3, false, true>(a, st);
-      else launch_quantize_t<kMxE4m3, false, false>(a, st);
-    }
+    if (x.f32)
+      return x.swiglu ? launch_quantize_t<kMxE8m0, true, true>(a, st)
+                      : launch_quantize_t<kMxE8m0, true, false>(a, st);
+    return x.swiglu ? launch_quantize_t<kMxE8m0, false, true>(a, st)
+                    : launch_quantize_t<kMxE8m0, false, false>(a, st);
   }
-  return cudaGetLastError();
+  if (x.f32)
+    return x.swiglu ? launch_quantize_t<kMxE4m3, true, true>(a, st)
+                    : launch_quantize_t<kMxE4m3, true, false>(a, st);
+  return x.swiglu ? launch_quantize_t<kMxE4m3, false, true>(a, st)
+                  : launch_quantize_t<kMxE4m3, false, false>(a, st);
 }
 
 cudaError_t launch_mx_dequant(const MxTensor& q, void* out, bool f32, int64_t ldo,
@@ -385,14 +399,9 @@ cudaError_t launch_mx_dequant(const MxTensor& q, void* out, bool f32, int64_t ld
   const DequantArgs a{q.codes, q.scales, q.row_scale, MxRows{q.offsets, q.groups, (int)q.rows},
                       (int)q.K, mx_tiles_k(q.fmt, q.K), out, ldo,
                       reinterpret_cast<uintptr_t>(out) % 32 == 0 && ldo * size % 32 == 0};
-  if (q.fmt == kMxE8m0) {
-    if (f32) launch_dequant_t<kMxE8m0, true>(a, st);
-    else launch_dequant_t<kMxE8m0, false>(a, st);
-  } else {
-    if (f32) launch_dequant_t<kMxE4m3, true>(a, st);
-    else launch_dequant_t<kMxE4m3, false>(a, st);
-  }
-  return cudaGetLastError();
+  if (q.fmt == kMxE8m0)
+    return f32 ? launch_dequant_t<kMxE8m0, true>(a, st) : launch_dequant_t<kMxE8m0, false>(a, st);
+  return f32 ? launch_dequant_t<kMxE4m3, true>(a, st) : launch_dequant_t<kMxE4m3, false>(a, st);
 }
 
 }  // namespace aaac
