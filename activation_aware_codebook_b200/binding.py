@@ -564,33 +564,58 @@ class MxTensor:
         if offsets is not None:
             _mx_offsets(offsets, groups)
         _mx_on(codes.get_device(), scales, row_scale, offsets)
-        self._set(codes, scales, row_scale, fmt, groups, offsets, rows, 2 * half)
+        self._codes, self._scales, self._row_scale = codes, scales, row_scale
+        self._set(fmt, groups, offsets, rows, 2 * half, codes.get_device(), codes.data_ptr(),
+                  scales.data_ptr(), None if row_scale is None else row_scale.data_ptr())
 
-    def _set(self, codes, scales, row_scale, fmt, groups, offsets, rows, K):
-        self.codes, self.scales, self.row_scale = codes, scales, row_scale
+    def _set(self, fmt, groups, offsets, rows, K, device, codes, scales, row_scale):
         self.fmt, self.groups, self.offsets = fmt, groups, offsets
-        self.rows, self.K = rows, K
-        self._c = CMxTensor(fmt, groups, rows, K, codes.data_ptr(), scales.data_ptr(),
-                            None if row_scale is None else row_scale.data_ptr(),
+        self.rows, self.K, self._device = rows, K, device
+        self._c = CMxTensor(fmt, groups, rows, K, codes, scales, row_scale,
                             None if offsets is None else offsets.data_ptr())
         self._ref = ctypes.byref(self._c)
 
+    # A tensor made by empty() keeps its parts in one allocation and cuts them
+    # out when they are asked for: decoding asks for none of them.
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            at, n = self._scale_bytes, self.rows * (self.K // 2)
+            self._codes = self._buffer[at:at + n].view(self.rows, self.K // 2)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            self._scales = self._buffer[:self._scale_bytes]
+        return self._scales
+
+    @property
+    def row_scale(self) -> Optional[torch.Tensor]:
+        if self._row_scale is None and self.fmt == MX_E4M3:
+            at = self._scale_bytes + self.rows * (self.K // 2)
+            self._row_scale = self._buffer[at:at + 4 * self.rows].view(torch.float32)
+        return self._row_scale
+
     @property
     def device(self):
-        return self.codes.device
+        return torch.device("cuda", self._device)
 
     @staticmethod
     def empty(fmt: int, rows: int, K: int, groups: int = 1,
               offsets: Optional[torch.Tensor] = None, device="cuda") -> "MxTensor":
-        need = _mx_bytes((_lib or load()).aaac_mx_scale_bytes, fmt, rows, K, groups)
+        size = _mx_bytes((_lib or load()).aaac_mx_scale_bytes, fmt, rows, K, groups)
         if offsets is not None:
             _mx_offsets(offsets, groups)
+        # scales (a multiple of 512 bytes), then codes (of 16 a row), then row scales
+        n = rows * (K // 2)
         t = object.__new__(MxTensor)
-        codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=device)
-        scales = torch.empty(need, dtype=torch.uint8, device=device)
-        row_scale = (torch.empty(rows, dtype=torch.float32, device=device) if fmt == MX_E4M3
-                     else None)
-        t._set(codes, scales, row_scale, fmt, groups, offsets, rows, K)
+        t._buffer = b = torch.empty(size + n + 4 * rows, dtype=torch.uint8, device=device)
+        t._scale_bytes = size
+        t._codes = t._scales = t._row_scale = None
+        at = b.data_ptr()
+        t._set(fmt, groups, offsets, rows, K, b.get_device(), at + size, at,
+               at + size + n if fmt == MX_E4M3 else None)
         return t
 
 
@@ -616,6 +641,11 @@ def _mx_on(device: int, *tensors) -> None:
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise ValueError(f"tensors on device {t.get_device()} and device {device}")
+
+
+def _mx_same(device: int, t: "MxTensor") -> None:
+    if t._device != device:
+        raise ValueError(f"tensors on device {t._device} and device {device}")
 
 
 def _mx_stream(device: int, stream) -> int:
@@ -688,11 +718,12 @@ def _mx_quantize(X, fmt, rows, swiglu, groups, offsets, out, stream):
     device = X.get_device()
     if out is None:
         _mx_on(device, rows, offsets)
-        out = MxTensor.empty(fmt, n, K, groups, offsets, X.device)
+        out = MxTensor.empty(fmt, n, K, groups, offsets, device)
     else:
         if (out.fmt, out.rows, out.K) != (fmt, n, K):
             raise ValueError(f"out is fmt {out.fmt} [{out.rows}, {out.K}], not {fmt} [{n}, {K}]")
-        _mx_on(device, rows, out.codes)
+        _mx_on(device, rows)
+        _mx_same(device, out)
     _check((_lib or load()).aaac_mx_quantize(ctypes.byref(src), out._ref,
                                              _mx_stream(device, stream)))
     return out
@@ -707,8 +738,8 @@ def mx_dequant(q: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = 
 
 
 def _mx_dequant(q, dtype, out, stream):
-    device = q.codes.get_device()
-    out, kind, ld = _mx_out(out, q.rows, q.K, dtype, q.codes.device)
+    device = q._device
+    out, kind, ld = _mx_out(out, q.rows, q.K, dtype, device)
     _mx_on(device, out)
     _check((_lib or load()).aaac_mx_dequant(q._ref, out.data_ptr(), kind, ld,
                                             _mx_stream(device, stream)))
@@ -738,9 +769,10 @@ def mx_linear(X: Union[torch.Tensor, MxTensor], W: MxTensor, out: Optional[torch
 
 
 def _mx_product(X, W, out, out_dtype, stream):
-    device = X.codes.get_device()
-    out, kind, ld = _mx_out(out, X.rows, W.rows // W.groups, out_dtype, X.codes.device)
-    _mx_on(device, W.codes, out)
+    device = X._device
+    _mx_same(device, W)
+    out, kind, ld = _mx_out(out, X.rows, W.rows // W.groups, out_dtype, device)
+    _mx_on(device, out)
     _check((_lib or load()).aaac_mx_linear(X._ref, W._ref, out.data_ptr(), kind, ld,
                                            _mx_stream(device, stream)))
     return out
@@ -751,16 +783,16 @@ def _mx_linear(X, W, out, out_dtype, rows, swiglu, offsets, ws, stream):
     device = X.get_device()
     if K != W.K:
         raise ValueError(f"X has K={K}, W has K={W.K}")
-    _mx_on(device, W.codes, rows, offsets, out, ws)
+    _mx_on(device, rows, offsets, out, ws)
+    _mx_same(device, W)
     if offsets is not None:
         _mx_offsets(offsets, W.groups)
-    where = X.device
-    out, kind, ld = _mx_out(out, n, W.rows // W.groups, out_dtype, where)
+    out, kind, ld = _mx_out(out, n, W.rows // W.groups, out_dtype, device)
     lib = _lib or load()
     if ws is None:
         # 0: the product quantises these rows itself (or refuses the sizes below)
         size = lib.aaac_mx_workspace_size(W.fmt, n, K, W.groups)
-        ws = torch.empty(size, dtype=torch.uint8, device=where) if size else None
+        ws = torch.empty(size, dtype=torch.uint8, device=device) if size else None
     else:
         size = ws.numel() * ws.element_size()
     _check(lib.aaac_mx_linear_ws(ctypes.byref(src), n,
