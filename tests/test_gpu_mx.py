@@ -474,6 +474,131 @@ def test_mixture_of_experts_block(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+def test_offsets_beyond_32_bits(fmt):
+    """2.3e9 values: codes past 2^30 bytes, activations past 2^32; the last rows
+    are those of the same rows alone, through every call."""
+    rows, K, N, tail = 70000, 32768, 40, 3
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    last = activations(tail, K, 8).cuda()
+    x[-tail:] = last
+    q, small = bb.mx_quantize(x, fmt), bb.mx_quantize(last, fmt)
+    assert torch.equal(q.codes[-tail:], small.codes)
+    W = bb.mx_quantize(synth.make_weight(N, K, 3).cuda(), fmt)
+    Y = bb.mx_linear(q, W)
+    assert not Y[:-tail].any()
+    check_product(bb.mx_linear(small, W), small, W, [0, tail], 1)
+    # the same products in another order of K may differ in their last bits
+    ref = bb.mx_linear(small, W)
+    S = bb.mx_linear(bb.mx_quantize(last.abs(), fmt),
+                     bb.mx_quantize(bb.mx_dequant(W).abs(), fmt))
+    assert (Y[-tail:] - ref).abs().le(2 * (K / 64 + 8) * 2.0 ** -23 * S + 1e-35).all()
+    del Y
+    back = bb.mx_dequant(q, out=x)
+    assert torch.equal(back[-tail:], bb.mx_dequant(small)) and not back[:100].any()
+
+
+def test_smallest_and_most_groups():
+    for fmt in FMTS:
+        x = activations(3, 32, 1).cuda()
+        W = bb.mx_quantize(activations(1, 32, 2).cuda(), fmt)
+        X = bb.mx_quantize(x, fmt)
+        check_product(bb.mx_linear(X, W), X, W, [0, 3], 1)
+        E, N, K, R = 1024, 3, 64, 300
+        W = bb.mx_quantize(synth.make_weight(E * N, K, 4).cuda(), fmt, groups=E)
+        cut = torch.sort(torch.randint(0, R + 1, (E + 1,), generator=torch.Generator().manual_seed(1))).values
+        off = cut.to(torch.int32).cuda()
+        x = activations(R, K, 5).cuda()
+        X = bb.mx_quantize(x, fmt, groups=E, offsets=off)
+        Y = torch.full((R, N), 4.0, device="cuda")
+        bb.mx_linear(X, W, out=Y)
+        torch.cuda.synchronize()
+        check_product(Y, X, W, cut.tolist(), E, y0=4.0)
+
+
+def test_offsets_that_are_not_sound_stay_inside():
+    """Offsets out of range or descending give unspecified rows; rows that other
+    tensors own are not touched."""
+    for fmt in FMTS:
+        E, N, K, R = 3, 70, 96, 50
+        W = bb.mx_quantize(synth.make_weight(E * N, K, 4).cuda(), fmt, groups=E)
+        for offsets in ([-5, 10, 20, 99], [40, 10, 30, 50], [60, 70, 80, 90], [0, 50, 0, 50]):
+            off = torch.tensor(offsets, dtype=torch.int32).cuda()
+            whole = torch.full((R + 20, N), 6.0, device="cuda")
+            bb.mx_linear(activations(R, K, 3).cuda(), W, out=whole[10:10 + R], offsets=off)
+            X = bb.mx_quantize(activations(R, K, 3).cuda(), fmt, groups=E, offsets=off)
+            bb.mx_dequant(X)
+            torch.cuda.synchronize()
+            assert (whole[:10] == 6.0).all() and (whole[10 + R:] == 6.0).all()
+    assert bb.device_timeouts() == 0
+
+
+def test_binding_refusals():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    W = bb.mx_quantize(x, bb.MX_E4M3)
+    W8 = bb.mx_quantize(x, bb.MX_E8M0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    bad = [lambda: bb.mx_quantize(x.half(), bb.MX_E4M3),
+           lambda: bb.mx_quantize(x[0], bb.MX_E4M3),
+           lambda: bb.mx_quantize(x.cpu(), bb.MX_E4M3),
+           lambda: bb.mx_quantize(x, bb.MX_E4M3, rows=torch.zeros(4, device="cuda")),
+           lambda: bb.mx_quantize(x, bb.MX_E4M3, groups=2, offsets=torch.zeros(2, **i32)),
+           lambda: bb.mx_quantize(x, bb.MX_E4M3, out=W8),
+           lambda: bb.mx_linear(W, W, rows=torch.zeros(4, **i32)),
+           lambda: bb.mx_linear(W, W, out=torch.zeros(4, 5, device="cuda")),
+           lambda: bb.mx_linear(W, W, out=torch.zeros(4, 4, dtype=torch.int32, device="cuda")),
+           lambda: bb.mx_linear(x[:, :32], W),
+           lambda: bb.mx_linear(x, W, rows=torch.zeros(4, dtype=torch.int32)),
+           lambda: bb.MxTensor(W.codes, W.scales[:-1], W.row_scale, bb.MX_E4M3),
+           lambda: bb.MxTensor(W.codes, W.scales, None, bb.MX_E4M3),
+           lambda: bb.MxTensor(W.codes.t(), W.scales, W.row_scale, bb.MX_E4M3)]
+    for f in bad:
+        with pytest.raises((ValueError, TypeError)):
+            f()
+    for f in (lambda: bb.mx_quantize(torch.zeros(4, 40, dtype=torch.bfloat16, device="cuda"), 0),
+              lambda: bb.mx_quantize(x, 2), lambda: bb.mx_linear(W8, W),
+              lambda: bb.mx_quantize(x, bb.MX_E4M3, groups=3)):
+        with pytest.raises(bb.AaacError):
+            f()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_captured_on_forked_streams(fmt):
+    """A capture that forks: one quantised input, three products on streams of
+    their own, joined again; replayed on new inputs."""
+    K, M = 384, 33
+    Ws = [bb.mx_quantize(synth.make_weight(n, K, n).cuda(), fmt) for n in (200, 64, 129)]
+    x = activations(M, K, 1).cuda()
+    X = bb.MxTensor.empty(fmt, M, K)
+    ys = [torch.zeros(M, W.rows, device="cuda") for W in Ws]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+
+    def step():
+        main = torch.cuda.current_stream()
+        bb.mx_quantize(x, fmt, out=X)
+        for s, W, y in zip(streams, Ws, ys):
+            s.wait_stream(main)
+            bb.mx_linear(X, W, out=y, stream=s)
+        for s in streams[:3]:
+            main.wait_stream(s)
+
+    with torch.cuda.stream(streams[3]):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=streams[3]):
+        step()
+    for seed in (2, 3):
+        new = activations(M, K, seed).cuda()
+        x.copy_(new)
+        for y in ys:
+            y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for y, W in zip(ys, Ws):
+            assert torch.equal(y, bb.mx_linear(bb.mx_quantize(new, fmt), W))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_streams_and_graphs(fmt):
     """Two streams with a workspace each, and a captured call replayed on new
     inputs and new expert counts."""
