@@ -553,7 +553,8 @@ class MxTensor:
         if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous():
             raise ValueError("codes must be contiguous uint8 [rows, K/2]")
         rows, half = codes.shape
-        need = _mx_bytes((_lib or load()).aaac_mx_scale_bytes, fmt, rows, 2 * half, groups)
+        # tiles of 128 rows x 4 blocks; every call checks the sizes themselves
+        need = (rows // 128 + groups) * -(-half // (64 if fmt == MX_E8M0 else 32)) * 512
         if scales.dtype != torch.uint8 or scales.numel() < need or not scales.is_contiguous():
             raise ValueError(f"scales must be contiguous uint8, {need} bytes")
         if fmt != MX_E4M3:
