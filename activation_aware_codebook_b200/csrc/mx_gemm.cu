@@ -19,11 +19,34 @@
 // The tensor core's N is the tile's own row count rounded up to 16, so a
 // ragged tile costs what its rows cost.
 //
-// SPLIT = false: persistent CTAs walk the tiles (weight-tile major inside a
-// group, so that CTAs in flight share weight rows in L2).  SPLIT = true: few
-// tiles; the CTAs of a cluster take a share of K each, and add their partial
-// tiles in rank order through distributed shared memory: the sum's order is
-// fixed, whatever the timing.
+// kWalk: persistent CTAs walk the tiles (weight-tile major inside a group, so
+// that CTAs in flight share weight rows in L2).  kPair: two CTAs walk tiles of
+// 256 weight rows together (cta_group::2); each holds its own weight rows and
+// half of the token rows, and the first issues the MMAs.  kSplit: few tiles;
+// the CTAs of a cluster take a share of K each, and add their partial tiles in
+// rank order through distributed shared memory: the sum's order is fixed,
+// whatever the timing.
+//
+// What bounds it (measured; times of a launch among others):
+//   14336 x 4096 at 8192 tokens, E4M3, bf16 out: 200 us, 4.8 PFLOP/s, 0.72 of
+//     four times the measured bf16 rate.  MMAs alone take 145 us, copies alone
+//     158: together they share shared memory (38 KB written and 32 KB read a
+//     CTA and stage of 512 MMA cycles, of 128 bytes a cycle) and the power
+//     limit (sw_power_cap: 245 us with its quantisation in a long run).
+//   5120 x 27648 at 333 tokens: 40 us, 0.31 us a stage of 37 KB, the way from
+//     L2 (copies alone 35).
+//   4096 x 4096 at one token: 7.1 us, of which 4.9 are a launch that loads and
+//     multiplies nothing.  64 experts of 2048 x 2048 at 128 rows: 22.6 us for
+//     133 MB, 0.9 of the measured HBM rate.
+// What was measured on the way: scale tiles by tcgen05.cp cost 41 ns each, in
+// line with the MMAs (12 a stage: 0.49 us of 0.88); as bulk copies of 2 KB they
+// cost 90 ns each to fetch, as tensor copies 18; a lane on its own in place of
+// a whole warp with one lane elected pays for every descriptor and coordinate
+// on its way to a uniform register (821 against 743 us at 2048 x 14336 x
+// 65536).  A ring of their own for the scale tiles, with a warp to fetch them,
+// was 5% slower; two sets of scale warps, or asking for the next stage before
+// its turn, changed nothing.
+//
 // A few rows that are not quantised yet (SRC: their kind; the single tokens of
 // decoding): eight more warps quantise each stage's columns straight into its
 // shared memory, as mx_quant.cu would, while the weights stream in: one
@@ -935,8 +958,8 @@ cudaError_t launch_f(const Maps& m, const MxGemmArgs& a, const MxPlan& p,
 // that split a tile run one after the other where there are too many of them,
 // each with its start, and its joining of the parts, 4 for every 256 columns.
 // Pairs of CTAs take tiles of twice the weight rows in the time of single
-// ones and with a third less traffic, as soon as there are tiles for all:
-// 2048 x 14336 x 16384 takes 189 us with them and 202 without, of which 0.93.
+// ones and with a third less traffic, as soon as there are tiles for all: 2048
+// tokens by 14336 x 16384 take 189 us with them and 202 without, hence 0.93.
 MxPlan mx_plan(int groups, int64_t rows, int64_t N, int64_t K) {
   MxPlan p;
   const int64_t stages = (K + kStageK - 1) / kStageK;

@@ -837,6 +837,9 @@ def run_linear(args):
     # context: cuBLAS bf16 (torch.matmul) on the dequantised weights, same
     # flush and timing, 4x the weight bytes
     W_hat = bb.dequant(packed, cfg, N, K).view(torch.bfloat16)
+    # beside it: the same layer in microscaled 4 bits (E2M1, E4M3 scales), with
+    # the activations quantised in the call (W4A4)
+    W_mx = bb.mx_quantize(W_hat, bb.MX_E4M3)
     points = []
     launches0 = bb.kernel_launches()
     sampler = ClockSampler(0)
@@ -870,6 +873,18 @@ def run_linear(args):
             if i >= args.warmup:
                 ctimes.append(e0.elapsed_time(e1))
         cublas_us = statistics.median(ctimes) * 1e3
+        need_mx = bb.mx_workspace_size(bb.MX_E4M3, M, K)
+        ws_mx = torch.empty(need_mx, dtype=torch.uint8, device=dev) if need_mx else None
+        mtimes = []
+        for i in range(args.warmup + args.steps):
+            flush.zero_()
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            e0.record(st)
+            bb.mx_linear(x, W_mx, out=Y, ws=ws_mx)
+            e1.record(st)
+            torch.cuda.synchronize()
+            if i >= args.warmup:
+                mtimes.append(e0.elapsed_time(e1))
         byts = code_bytes + M * K * 2 + M * N * 4
         flops = 2.0 * M * N * K
         if M <= 64:
@@ -884,7 +899,8 @@ def run_linear(args):
                 else "tcgen05 fused expansion" if not need else "dequant + TMA-fed tcgen05")
         points.append({"tokens": M, "us": ms * 1e3, "tokens_per_s": M / (ms * 1e-3),
                        "path": path, "roofline": roof,
-                       "cublas_bf16_dequantised_us": cublas_us})
+                       "cublas_bf16_dequantised_us": cublas_us,
+                       "microscaled_w4a4_us": statistics.median(mtimes) * 1e3})
     clocks = sampler.stop()
     launches = bb.kernel_launches() - launches0
     head = points[0]
