@@ -174,7 +174,7 @@ def load(path: str = LIB_PATH):
     L.aaac_mx_linear.restype = ctypes.c_int
     L.aaac_mx_linear.argtypes = [P, P, P, i32, i64, P]
     L.aaac_mx_workspace_size.restype = sz
-    L.aaac_mx_workspace_size.argtypes = [i32, i64, i64, i32]
+    L.aaac_mx_workspace_size.argtypes = [i32, i64, i64, i32, u32]
     L.aaac_mx_linear_ws.restype = ctypes.c_int
     L.aaac_mx_linear_ws.argtypes = [P, i64, P, P, P, i32, i64, P, sz, P]
     L.aaac_mx_launch_plan.restype = ctypes.c_int
@@ -528,10 +528,10 @@ def mx_scale_bytes(fmt: int, rows: int, K: int, groups: int = 1) -> int:
     return int(load().aaac_mx_scale_bytes(fmt, rows, K, groups))
 
 
-def mx_workspace_size(fmt: int, rows: int, K: int, groups: int = 1) -> int:
+def mx_workspace_size(fmt: int, rows: int, K: int, groups: int = 1, swiglu: bool = False) -> int:
     """Bytes of the workspace in which mx_linear quantises its activations (0
     for the few rows that the product's kernel quantises itself)."""
-    return int(load().aaac_mx_workspace_size(fmt, rows, K, groups))
+    return int(load().aaac_mx_workspace_size(fmt, rows, K, groups, MX_SWIGLU if swiglu else 0))
 
 
 def mx_launch_plan(groups: int, rows: int, N: int, K: int) -> dict:
@@ -792,7 +792,7 @@ def _mx_linear(X, W, out, out_dtype, rows, swiglu, offsets, ws, stream):
     lib = _lib or load()
     if ws is None:
         # 0: the product quantises these rows itself (or refuses the sizes below)
-        size = lib.aaac_mx_workspace_size(W.fmt, n, K, W.groups)
+        size = lib.aaac_mx_workspace_size(W.fmt, n, K, W.groups, src.flags)
         ws = torch.empty(size, dtype=torch.uint8, device=device) if size else None
     else:
         size = ws.numel() * ws.element_size()

@@ -764,8 +764,11 @@ aaac_status aaac_mx_linear(const aaac_mx_tensor* x, const aaac_mx_tensor* w, voi
                    "aaac_mx_linear");
 }
 
-size_t aaac_mx_workspace_size(int32_t fmt, int64_t rows, int64_t K, int32_t groups) {
-  if (check_mx_shape(fmt, rows, K, groups) != AAAC_OK || aaac::mx_own_rows(groups, rows, K)) return 0;
+size_t aaac_mx_workspace_size(int32_t fmt, int64_t rows, int64_t K, int32_t groups,
+                              uint32_t flags) {
+  if (check_mx_shape(fmt, rows, K, groups) != AAAC_OK ||
+      aaac::mx_own_rows(fmt, groups, rows, K, (flags & AAAC_MX_SWIGLU) != 0))
+    return 0;
   return aaac::align256((size_t)rows * (size_t)(K / 2)) +
          aaac::align256(aaac::mx_scale_bytes(fmt, rows, K, groups)) +
          aaac::align256((size_t)rows * sizeof(float));
@@ -784,9 +787,11 @@ aaac_status aaac_mx_linear_ws(const aaac_mx_source* src, int64_t rows, const int
   if (!aligned4(offsets)) return fail(AAAC_ERR_ALIGN, "offsets is not 4-byte aligned");
   CHECK(check_mx_source(src, rows, w->K));
   CHECK(check_mx_out(Y, type, ldy, w->rows / w->groups, rows, 1));
-  const bool own = aaac::mx_own_rows(w->groups, rows, w->K);
+  const bool own = aaac::mx_own_rows(w->fmt, w->groups, rows, w->K,
+                                     (src->flags & AAAC_MX_SWIGLU) != 0);
   if (rows > 0 && !own)
-    CHECK(check_ws(ws, ws_bytes, aaac_mx_workspace_size(w->fmt, rows, w->K, w->groups)));
+    CHECK(check_ws(ws, ws_bytes,
+                   aaac_mx_workspace_size(w->fmt, rows, w->K, w->groups, src->flags)));
   CHECK(take_fault());
   if (rows == 0) return ok();
   const aaac::MxSource source = mx_source_of(src);

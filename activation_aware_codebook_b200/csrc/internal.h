@@ -169,7 +169,7 @@ cudaError_t launch_mx_quantize(const MxSource& x, const MxTensor& q, cudaStream_
 cudaError_t launch_mx_dequant(const MxTensor& q, void* out, bool f32, int64_t ldo,
                               cudaStream_t st);
 // whether the product takes these rows as they are and quantises them itself
-bool mx_own_rows(int groups, int64_t rows, int64_t K);
+bool mx_own_rows(int fmt, int groups, int64_t rows, int64_t K, bool swiglu);
 // src: rows that it quantises itself (x has no codes then), or NULL;
 // overlap: the kernel before it on the stream is launch_mx_quantize's, and
 // everything but its outputs was ready before that one started

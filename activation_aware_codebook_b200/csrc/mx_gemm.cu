@@ -98,7 +98,7 @@ struct RowsArgs {
   int warps;          // warps of a stage: two rows each, a power of two
 };
 constexpr int kSrcNone = -1, kSrcBf16 = 0, kSrcF32 = 1, kSrcBf16Glu = 2, kSrcF32Glu = 3;
-constexpr int kMaxOwnRows = 16;
+constexpr int kMaxOwnRows = 8;
 constexpr int kOwnWarps = 8;
 
 // How the CTAs of a launch share the work.
@@ -579,25 +579,32 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       return src >= 0 && src < own.src_rows ? (int64_t)src * own.ldx : -1;
     };
     if (FMT == kMxE4m3) {
-      const int runs = a.K >> 4;
-      for (int i0 = ow * 32; i0 < count * runs; i0 += kOwnWarps * 32) {
-        const int i = i0 + lane;
-        const int r = min(i, count * runs - 1) / runs;
-        uint32_t m = 0u;
-        if (i < count * runs) {
-          const int64_t at = row_start(r);
-          if (at >= 0) {
-            Run<kF32, kGlu> run;
-            run.load(own.X, at, (i - r * runs) * 16, a.K);
-            m = run.amax();
-          }
+      // the rows' largest magnitudes: kBatch runs a lane, their loads together
+      constexpr int kBatch = kF32 || kGlu ? 2 : 4;
+      const int runs = a.K >> 4, all = count * runs;
+      for (int i0 = ow * 32; i0 < all; i0 += kBatch * kOwnWarps * 32) {
+        Run<kF32, kGlu> run[kBatch];
+        int row[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; u++) {
+          const int i = i0 + u * kOwnWarps * 32 + lane;
+          row[u] = min(i, all - 1) / runs;
+          const int64_t at = row_start(row[u]);
+          if (i < all && at >= 0) run[u].load(own.X, at, (i - row[u] * runs) * 16, a.K);
+          else run[u].zero();
         }
-        const int r0 = __shfl_sync(0xffffffffu, r, 0), r1 = __shfl_sync(0xffffffffu, r, 31);
-        if (r0 == r1) {
-          m = __reduce_max_sync(0xffffffffu, m);
-          if (lane == 0) atomicMax(&s_top[r0], m);
-        } else {
-          atomicMax(&s_top[r], m);
+#pragma unroll
+        for (int u = 0; u < kBatch; u++) {
+          if (i0 + u * kOwnWarps * 32 >= all) continue;  // warp-uniform
+          uint32_t m = run[u].amax();
+          const int r0 = __shfl_sync(0xffffffffu, row[u], 0);
+          const int r1 = __shfl_sync(0xffffffffu, row[u], 31);
+          if (r0 == r1) {
+            m = __reduce_max_sync(0xffffffffu, m);
+            if (lane == 0) atomicMax(&s_top[r0], m);
+          } else {
+            atomicMax(&s_top[row[u]], m);
+          }
         }
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kOwnWarps * 32) : "memory");
@@ -620,31 +627,35 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                         (uint32_t)((((j >> 1) ^ (r & 7)) << 4) + (j & 1) * 8);
     const int block = FMT == kMxE8m0 ? j >> 1 : j;
     const uint32_t scale_to = (uint32_t)((block >> 2) * kMxTileBytes + r * 16 + (block & 3));
-    Ring<S::kStages> ring;
-    bool ok = true;
-    int it = 0;
-    for (int item = item0; item < items && ok; item += step) {
-      for (int st = st_lo; st < st_hi; st++, it++, ring.next()) {
-        if (it % sets != set) continue;
-        const int col = st * kStageK + j * 16;
-        Run<kF32, kGlu> run;
-        if (at >= 0 && col < a.K) run.load(own.X, at, col, a.K);
-        else run.zero();
-        if (it >= S::kStages) ok = warp_wait(&empty[ring.s], ring.phase ^ 1);
-        if (!ok) {
-          s_fail = 1;
-          break;
-        }
-        uint32_t c[2];
-        const uint32_t byte = encode<FMT>(run, down, bad_row, c);
-        *reinterpret_cast<uint2*>(sX + ring.s * S::kXTile + to) = make_uint2(c[0], c[1]);
-        if (FMT == kMxE4m3 || (j & 1) == 0)
-          sSX[ring.s * S::kSub * S::kScale + scale_to] = (unsigned char)byte;
-        fence_proxy_async();  // generic-proxy stores -> visible to the tensor core
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[ring.s]);
+    // all its stages, over the tiles; the next one's run is fetched before this
+    // one waits for its stage
+    const int tiles = item0 >= items ? 0 : (SPLIT ? 1 : (items - item0 + step - 1) / step);
+    const int total = tiles * nst;
+    int st = st_lo + set % max(nst, 1);
+    auto fetch = [&](Run<kF32, kGlu>& run) {
+      const int col = st * kStageK + j * 16;
+      if (at >= 0 && col < a.K) run.load(own.X, at, col, a.K);
+      else run.zero();
+    };
+    Run<kF32, kGlu> run, next;
+    if (set < total) fetch(next);
+    for (int it = set; it < total; it += sets) {
+      run = next;
+      for (st += sets; st >= st_hi;) st -= nst;
+      if (it + sets < total) fetch(next);
+      const int s = it % S::kStages;
+      if (it >= S::kStages && !warp_wait(&empty[s], ((it / S::kStages) - 1) & 1)) {
+        s_fail = 1;
+        break;
       }
-      if (SPLIT) break;
+      uint32_t c[2];
+      const uint32_t byte = encode<FMT>(run, down, bad_row, c);
+      *reinterpret_cast<uint2*>(sX + s * S::kXTile + to) = make_uint2(c[0], c[1]);
+      if (FMT == kMxE4m3 || (j & 1) == 0)
+        sSX[s * S::kSub * S::kScale + scale_to] = (unsigned char)byte;
+      fence_proxy_async();  // generic-proxy stores -> visible to the tensor core
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
     }
   } else {
     after_previous();  // the row scales
@@ -930,14 +941,16 @@ cudaError_t launch_own(const Maps& m, const MxGemmArgs& a, const MxPlan& p, cons
                      : launch_t<FMT, 32, kWalk, SRC>(m, a, p, st, own);
 }
 
-template <int FMT>
-cudaError_t launch_own_f(const Maps& m, const MxGemmArgs& a, const MxPlan& p, const MxSource& x,
-                         const RowsArgs& own, cudaStream_t st) {
-  if (x.f32)
-    return x.swiglu ? launch_own<FMT, kSrcF32Glu>(m, a, p, own, st)
-                    : launch_own<FMT, kSrcF32>(m, a, p, own, st);
-  return x.swiglu ? launch_own<FMT, kSrcBf16Glu>(m, a, p, own, st)
-                  : launch_own<FMT, kSrcBf16>(m, a, p, own, st);
+cudaError_t launch_own_s(int fmt, const Maps& m, const MxGemmArgs& a, const MxPlan& p,
+                         const MxSource& x, const RowsArgs& own, cudaStream_t st) {
+  if (fmt == kMxE4m3)  // no SwiGLU (mx_own_rows)
+    return x.f32 ? launch_own<kMxE4m3, kSrcF32>(m, a, p, own, st)
+                 : launch_own<kMxE4m3, kSrcBf16>(m, a, p, own, st);
+  if (x.swiglu)
+    return x.f32 ? launch_own<kMxE8m0, kSrcF32Glu>(m, a, p, own, st)
+                 : launch_own<kMxE8m0, kSrcBf16Glu>(m, a, p, own, st);
+  return x.f32 ? launch_own<kMxE8m0, kSrcF32>(m, a, p, own, st)
+               : launch_own<kMxE8m0, kSrcBf16>(m, a, p, own, st);
 }
 
 template <int FMT>
@@ -1008,10 +1021,19 @@ MxPlan mx_plan(int groups, int64_t rows, int64_t N, int64_t K) {
   return p;
 }
 
-// Few rows, and short: every CTA quantises its part of them itself (and reads
-// all of them for the rows' maxima).
-bool mx_own_rows(int groups, int64_t rows, int64_t K) {
-  return groups == 1 && rows <= kMaxOwnRows && rows * K <= 32768;
+// The few rows that every CTA quantises itself, its part of K at a time; for
+// E4M3 it first reads all of them for their maxima.  Measured against the
+// quantisation in a launch before (us, of calls in a row in a graph):
+//   E8M0  4096 x 4096, 1 row 6.6 (7.4), 8 rows 7.0 (7.6), 16 rows 7.5 (7.8);
+//         5120 x 27648, 1 row 14.5 (16.9), 8 rows 15.8 (17.0), 16 rows 21.9 (17.3);
+//         SwiGLU 14336 x 4096, 1 row 8.2 (8.8), 4 rows 8.7 (8.8), 8 rows 11.5 (8.8)
+//   E4M3  14336 x 4096, 1 row 8.3 (9.0), 2 rows 8.9 (9.0), 4 rows 9.6 (9.0);
+//         4096 x 14336, 1 row 11.5 (10.5); SwiGLU 4096 x 4096, 1 row 8.7 (7.8)
+// and about 4 us less of the host's time.
+bool mx_own_rows(int fmt, int groups, int64_t rows, int64_t K, bool swiglu) {
+  if (groups != 1) return false;
+  if (fmt == kMxE8m0) return rows <= (swiglu ? kMaxOwnRows / 2 : kMaxOwnRows);
+  return !swiglu && rows <= kMaxOwnRows && rows * K <= 8192;
 }
 
 cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f32, int64_t ldy,
@@ -1036,8 +1058,7 @@ cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f
     int warps = 1;
     while (2 * warps < (int)x.rows) warps *= 2;
     const RowsArgs own{src->X, src->index, src->ldx, (int)src->rows, warps};
-    return x.fmt == kMxE8m0 ? launch_own_f<kMxE8m0>(m, a, p, *src, own, st)
-                            : launch_own_f<kMxE4m3>(m, a, p, *src, own, st);
+    return launch_own_s(x.fmt, m, a, p, *src, own, st);
   }
   return x.fmt == kMxE8m0 ? launch_f<kMxE8m0>(m, a, p, st)
                           : launch_f<kMxE4m3>(m, a, p, st);

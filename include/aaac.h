@@ -427,12 +427,14 @@ aaac_status aaac_mx_linear(const aaac_mx_tensor* x, const aaac_mx_tensor* w, voi
 /* aaac_mx_quantize and aaac_mx_linear in one call: Y from bf16 or fp32
  * activations, the same bits as the two calls.  They are quantised into the
  * workspace, and the product's kernel sets itself up and fetches its first
- * weights meanwhile; up to 16 rows of one group (rows * K <= 32768) the
- * product's kernel quantises itself, for which aaac_mx_workspace_size returns
- * 0 and ws may be NULL.  rows and offsets are those of the quantised tensor
- * (offsets NULL: equal groups).
- *   ws   device, aaac_mx_workspace_size(w->fmt, rows, w->K, w->groups) bytes */
-size_t aaac_mx_workspace_size(int32_t fmt, int64_t rows, int64_t K, int32_t groups);
+ * weights meanwhile; a few rows of one group (up to 8, as the library chooses)
+ * the product's kernel quantises itself, for which aaac_mx_workspace_size
+ * returns 0 and ws may be NULL.  rows and offsets are those of the quantised
+ * tensor (offsets NULL: equal groups).
+ *   ws   device, aaac_mx_workspace_size(w->fmt, rows, w->K, w->groups,
+ *        src->flags) bytes */
+size_t aaac_mx_workspace_size(int32_t fmt, int64_t rows, int64_t K, int32_t groups,
+                              uint32_t flags);
 aaac_status aaac_mx_linear_ws(const aaac_mx_source* src, int64_t rows, const int32_t* offsets,
                               const aaac_mx_tensor* w, void* Y, int32_t type, int64_t ldy,
                               void* ws, size_t ws_bytes, void* stream);
