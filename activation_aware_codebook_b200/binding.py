@@ -723,6 +723,9 @@ def _mx_quantize(X, fmt, rows, swiglu, groups, offsets, out, stream):
     else:
         if (out.fmt, out.rows, out.K) != (fmt, n, K):
             raise ValueError(f"out is fmt {out.fmt} [{out.rows}, {out.K}], not {fmt} [{n}, {K}]")
+        if (groups not in (1, out.groups)
+                or (offsets is not None and offsets is not out.offsets)):
+            raise ValueError("out has its own groups and offsets")
         _mx_on(device, rows)
         _mx_same(device, out)
     _check((_lib or load()).aaac_mx_quantize(ctypes.byref(src), out._ref,

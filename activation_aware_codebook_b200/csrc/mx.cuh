@@ -37,12 +37,43 @@ struct MxRows {
   int rows;  // of all groups
 };
 
+// Global loads of what an earlier kernel on the stream may have written while
+// this one was already there (see after_previous): ordered behind the wait, and
+// not through the path for data that is constant over a kernel's lifetime.
+__device__ __forceinline__ int32_t load_i32(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_u8(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float load_f32(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 load_2(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 load_4(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // Group e's rows [first, last), held inside the tensor whatever the offsets say.
 __device__ __forceinline__ void mx_group(const MxRows& g, int e, int* first, int* last) {
   if (g.offsets) {
-    const int a = min(max(__ldg(g.offsets + e), 0), g.rows);
+    const int a = min(max(load_i32(g.offsets + e), 0), g.rows);
     *first = a;
-    *last = min(max(__ldg(g.offsets + e + 1), a), g.rows);
+    *last = min(max(load_i32(g.offsets + e + 1), a), g.rows);
   } else {
     const int per = g.rows / g.groups;
     *first = e * per;

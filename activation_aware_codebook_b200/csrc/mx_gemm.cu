@@ -575,7 +575,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     // where the group's row r starts in X; -1: a row of zeros
     auto row_start = [&](int r) -> int64_t {
       if (r >= count) return -1;
-      const int src = own.index ? __ldg(own.index + first + r) : first + r;
+      const int src = own.index ? load_i32(own.index + first + r) : first + r;
       return src >= 0 && src < own.src_rows ? (int64_t)src * own.ldx : -1;
     };
     if (FMT == kMxE4m3) {
@@ -675,13 +675,13 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       const int mine = t.count - part * NC;  // this warp's tokens
       float gw = 1.0f;
       if (FMT == kMxE4m3 && !SPLIT) {  // fetched while the MMAs run
-        if (nok) gw = __ldg(a.gw + (int64_t)t.e * a.N + n);
+        if (nok) gw = load_f32(a.gw + (int64_t)t.e * a.N + n);
         if (!S::kOwn) {
           __syncwarp();
 #pragma unroll
           for (int c = 0; c < NC; c += 32)
             if (c + lane < NC)
-              gx[c + lane] = c + lane < mine ? __ldg(a.gx + t.row + part * NC + c + lane) : 0.0f;
+              gx[c + lane] = c + lane < mine ? load_f32(a.gx + t.row + part * NC + c + lane) : 0.0f;
           __syncwarp();
         }
       }
@@ -825,11 +825,11 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
             v[3] = __fadd_rn(v[3], part[k].w);
           }
         if (FMT == kMxE4m3) {
-          const float g = S::kOwn ? s_scale[c] : __ldg(a.gx + t.row + c);
+          const float g = S::kOwn ? s_scale[c] : load_f32(a.gx + t.row + c);
           const float* gw = a.gw + (int64_t)t.e * a.N;
 #pragma unroll
           for (int j = 0; j < 4; j++)
-            v[j] = __fmul_rn(__fmul_rn(v[j], g), n + j < a.N ? __ldg(gw + n + j) : 0.0f);
+            v[j] = __fmul_rn(__fmul_rn(v[j], g), n + j < a.N ? load_f32(gw + n + j) : 0.0f);
         }
         const int64_t y = (int64_t)(t.row + c) * a.ldy + n;
         if (a.bf16_out) {

@@ -66,12 +66,12 @@ struct QuantArgs {
 __device__ __forceinline__ int group_of(const MxRows& g, int r, int lane) {
   int e = 0;
   for (int i = 1; i <= g.groups; i += 32) {
-    const bool before = i + lane <= g.groups && __ldg(g.offsets + min(i + lane, g.groups)) <= r;
+    const bool before = i + lane <= g.groups && load_i32(g.offsets + min(i + lane, g.groups)) <= r;
     const unsigned b = __ballot_sync(0xffffffffu, before);
     e += __popc(b);
     if (b != 0xffffffffu) break;
   }
-  return e >= g.groups || r < __ldg(g.offsets) ? -1 : e;
+  return e >= g.groups || r < load_i32(g.offsets) ? -1 : e;
 }
 
 // Where row r of group e, whose first row is `first`, keeps its scale bytes (of
@@ -125,7 +125,7 @@ quantize_kernel(const __grid_constant__ QuantArgs a) {
   let_next_start();
   const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int T = blockDim.x;
-  const int src = a.index ? __ldg(a.index + row) : row;
+  const int src = a.index ? load_i32(a.index + row) : row;
   const bool have = src >= 0 && src < a.src_rows;
   const int64_t row_at = (int64_t)(have ? src : 0) * a.ldx;
   const int runs = a.K >> 4;
@@ -321,9 +321,9 @@ mx_dequant_kernel(const __grid_constant__ DequantArgs a, int row0, uint32_t tota
     row[u] = row0 + (int)r;
     run[u] = (int)(i - r * runs.d);
     const uint8_t* srow = a.scales + scale_equal(per, (uint32_t)row[u], a.tiles_k);
-    w[u] = __ldg(reinterpret_cast<const uint2*>(a.codes + (int64_t)row[u] * (a.K >> 1)) + run[u]);
-    sb[u] = __ldg(srow + scale_step<FMT>(run[u]));
-    g[u] = FMT == kMxE4m3 ? __ldg(a.row_scale + row[u]) : 1.0f;
+    w[u] = load_2(reinterpret_cast<const uint2*>(a.codes + (int64_t)row[u] * (a.K >> 1)) + run[u]);
+    sb[u] = load_u8(srow + scale_step<FMT>(run[u]));
+    g[u] = FMT == kMxE4m3 ? load_f32(a.row_scale + row[u]) : 1.0f;
   }
 #pragma unroll
   for (int u = 0; u < kDeqRuns; u++) {
@@ -345,11 +345,11 @@ mx_dequant_ragged_kernel(const __grid_constant__ DequantArgs a) {
   if (at < 0) return;
   const uint2* crow = reinterpret_cast<const uint2*>(a.codes + (int64_t)row * (a.K >> 1));
   const uint8_t* srow = a.scales + at;
-  const float g = FMT == kMxE4m3 ? __ldg(a.row_scale + row) : 1.0f;
+  const float g = FMT == kMxE4m3 ? load_f32(a.row_scale + row) : 1.0f;
 #pragma unroll 2
   for (int i = threadIdx.x; i < (a.K >> 4); i += blockDim.x) {
     float v[16];
-    expand16(__ldg(crow + i), scale_value<FMT>(__ldg(srow + scale_step<FMT>(i)), g), v);
+    expand16(load_2(crow + i), scale_value<FMT>(load_u8(srow + scale_step<FMT>(i)), g), v);
     store16<F32>(a.out, row * a.ldo + 16 * (int64_t)i, v, a.wide);
   }
 }

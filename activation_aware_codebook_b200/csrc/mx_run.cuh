@@ -45,20 +45,20 @@ struct Run {
   }
   __device__ __forceinline__ static void load16(const void* X, int64_t at, float (&o)[16]) {
     if (F32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(X) + at);
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(X) + at);
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const float4 q = __ldg(p + i);
-        o[4 * i] = q.x;
-        o[4 * i + 1] = q.y;
-        o[4 * i + 2] = q.z;
-        o[4 * i + 3] = q.w;
+        const uint4 q = load_4(p + i);
+        o[4 * i] = __uint_as_float(q.x);
+        o[4 * i + 1] = __uint_as_float(q.y);
+        o[4 * i + 2] = __uint_as_float(q.z);
+        o[4 * i + 3] = __uint_as_float(q.w);
       }
     } else {
       const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(X) + at);
 #pragma unroll
       for (int i = 0; i < 2; i++) {
-        const uint4 q = __ldg(p + i);
+        const uint4 q = load_4(p + i);
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int j = 0; j < 4; j++) {
@@ -105,7 +105,7 @@ struct Run<false, false> {
   }
   __device__ __forceinline__ void load(const void* X, int64_t row_at, int col, int) {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(X) + row_at + col);
-    const uint4 a = __ldg(p), b = __ldg(p + 1);
+    const uint4 a = load_4(p), b = load_4(p + 1);
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }

@@ -353,7 +353,7 @@ def test_group_rows_do_not_depend_on_their_batch(fmt):
 @pytest.mark.parametrize("rows,K,N", [(1, 32, 130), (1, 4096, 300), (2, 2080, 70), (3, 544, 128),
                                       (5, 1056, 200), (8, 288, 129), (16, 2048, 260),
                                       (4, 96, 128 * 151), (1, 32768, 128), (7, 1152, 128 * 150),
-                                      (4, 8224, 128 * 149)])
+                                      (4, 2336, 128 * 149)])
 def test_few_rows_are_quantised_by_the_product(fmt, dtype, swiglu, rows, K, N):
     """A few rows are quantised by the product itself: the same bits as
     quantisation and product, for K split over CTAs, whole, and for CTAs with
@@ -546,6 +546,8 @@ def test_binding_refusals():
            lambda: bb.mx_quantize(x, bb.MX_E4M3, rows=torch.zeros(4, device="cuda")),
            lambda: bb.mx_quantize(x, bb.MX_E4M3, groups=2, offsets=torch.zeros(2, **i32)),
            lambda: bb.mx_quantize(x, bb.MX_E4M3, out=W8),
+           lambda: bb.mx_quantize(x, bb.MX_E4M3, out=W, groups=2),
+           lambda: bb.mx_quantize(x, bb.MX_E4M3, out=W, offsets=torch.zeros(2, **i32)),
            lambda: bb.mx_linear(W, W, rows=torch.zeros(4, **i32)),
            lambda: bb.mx_linear(W, W, out=torch.zeros(4, 5, device="cuda")),
            lambda: bb.mx_linear(W, W, out=torch.zeros(4, 4, dtype=torch.int32, device="cuda")),
