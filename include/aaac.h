@@ -358,8 +358,8 @@ aaac_status aaac_linear_ws(const void* X, int64_t M, int64_t ldx, const uint8_t*
  * Rows come in `groups` groups (an expert's rows each): of equal size when
  * offsets is NULL, else rows offsets[e] .. offsets[e + 1] - 1 are group e's
  * (device int32 [groups + 1], ascending; groups may be empty; rows before
- * offsets[0] or from offsets[groups] on belong to none, and no call reads or
- * writes them).  Values of offsets outside [0, rows] are taken as the nearest
+ * offsets[0] or from offsets[groups] on belong to none: no call writes
+ * anything of theirs, and nothing depends on them).  Values of offsets outside [0, rows] are taken as the nearest
  * bound; descending ones give unspecified values, and every access stays in
  * bounds.
  *   codes      [rows][K/2]: two per byte, low nibble = even k
