@@ -18,9 +18,9 @@
 // maximum and its codes, so a row is read once; a run is one E4M3 block, and
 // half an E8M0 one.  2 bytes in, 0.53 (E8M0) or 0.56 (E4M3) out per value.
 // Measured with a cold L2, of 6.55 TB/s: 8192 x 14336 bf16 to E8M0 53 us (5.6
-// TB/s), to E4M3 59 us (5.1 TB/s: the instructions, 63% of the ALU pipe).
-// SwiGLU of 4099 x 2 x 8192 to E4M3 45 us (3.4 TB/s): 33 instructions a value,
-// most of them expf and the divisions.
+// TB/s), to E4M3 56 us (5.3 TB/s).  SwiGLU of 4099 x 2 x 8192 to E4M3 44 us (3.5
+// TB/s): 29 instructions a value, most of them expf, the divisions and unpacking;
+// they keep the issue slots 77% busy.
 // mx_dequant_kernel: 27648 x 5120 from E4M3 to bf16 59 us (6.1 TB/s).
 #include "common.cuh"
 #include "internal.h"

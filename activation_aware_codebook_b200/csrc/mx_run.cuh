@@ -28,11 +28,52 @@ __device__ __forceinline__ float div_by(float x, float d, float r) {
   return __fmaf_rn(-r, __fmaf_rn(d, q, -x), q);  // these signs keep a zero's
 }
 
-// silu(a) b, each step in fp32.  exp(-a) is held below 2^126, so that its
-// reciprocal is a normal number: silu(a) is below 1e-35 there.
-__device__ __forceinline__ float silu_mul(float a, float b) {
-  const float d = __fadd_rn(1.0f, expf(fminf(-a, 87.0f)));
-  return __fmul_rn(div_by(a, d, rcp_approx(d)), b);
+// Two values in a register pair: one instruction does for both what the scalar
+// one does for each, rounded alike (SwiGLU of 65536 x 2 x 2048 to E4M3: 148 us
+// in scalars, 134 in pairs).
+struct Two {
+  uint64_t p;
+  __device__ __forceinline__ Two(float a, float b) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+  }
+  __device__ __forceinline__ explicit Two(float a) : Two(a, a) {}
+  __device__ __forceinline__ explicit Two(uint64_t p_) : p(p_) {}
+  __device__ __forceinline__ void get(float& a, float& b) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+  }
+};
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.p), "l"(b.p));
+  return Two(r);
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.p), "l"(b.p));
+  return Two(r);
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.p), "l"(b.p), "l"(c.p));
+  return Two(r);
+}
+
+// div_by of two values and with every sign turned, -(x / d) with nr = -r: a
+// pair has no negated operands.
+__device__ __forceinline__ Two neg_div_by(Two x, Two d, Two nr) {
+  const Two q = mul2(x, nr);
+  return fma2(nr, fma2(d, q, x), q);
+}
+
+// silu(a) b for two columns, each step in fp32; na = -a.  exp(-a) is held below
+// 2^126, so that its reciprocal is a normal number: silu(a) is below 1e-35 there.
+__device__ __forceinline__ void silu_mul(float na0, float na1, float b0, float b1, float& y0,
+                                         float& y1) {
+  const Two d = add2(Two(1.0f), Two(expf(fminf(na0, 87.0f)), expf(fminf(na1, 87.0f))));
+  float d0, d1;
+  d.get(d0, d1);
+  const Two nr(-rcp_approx(d0), -rcp_approx(d1));
+  mul2(neg_div_by(Two(na0, na1), d, nr), Two(b0, b1)).get(y0, y1);
 }
 
 // 16 values of a row.  bf16 stays packed: half the registers.
@@ -43,25 +84,28 @@ struct Run {
 #pragma unroll
     for (int i = 0; i < 16; i++) v[i] = 0.0f;
   }
+  // NEG: with the signs turned
+  template <bool NEG>
   __device__ __forceinline__ static void load16(const void* X, int64_t at, float (&o)[16]) {
     if (F32) {
       const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(X) + at);
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const uint4 q = load_4(p + i);
-        o[4 * i] = __uint_as_float(q.x);
-        o[4 * i + 1] = __uint_as_float(q.y);
-        o[4 * i + 2] = __uint_as_float(q.z);
-        o[4 * i + 3] = __uint_as_float(q.w);
+        o[4 * i] = __uint_as_float(q.x ^ (NEG ? 0x80000000u : 0u));
+        o[4 * i + 1] = __uint_as_float(q.y ^ (NEG ? 0x80000000u : 0u));
+        o[4 * i + 2] = __uint_as_float(q.z ^ (NEG ? 0x80000000u : 0u));
+        o[4 * i + 3] = __uint_as_float(q.w ^ (NEG ? 0x80000000u : 0u));
       }
     } else {
       const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(X) + at);
 #pragma unroll
       for (int i = 0; i < 2; i++) {
         const uint4 q = load_4(p + i);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int j = 0; j < 4; j++) {
+          if (NEG) w[j] ^= 0x80008000u;
           o[8 * i + 2 * j] = bf16_lo(w[j]);
           o[8 * i + 2 * j + 1] = bf16_hi(w[j]);
         }
@@ -70,12 +114,13 @@ struct Run {
   }
   // row_at: the source row's first element; col: this run's first column
   __device__ __forceinline__ void load(const void* X, int64_t row_at, int col, int K) {
-    load16(X, row_at + col, v);
+    load16<SWIGLU>(X, row_at + col, v);
     if (SWIGLU) {
       float u[16];
-      load16(X, row_at + K + col, u);
+      load16<false>(X, row_at + K + col, u);
 #pragma unroll
-      for (int i = 0; i < 16; i++) v[i] = silu_mul(v[i], u[i]);
+      for (int i = 0; i < 16; i += 2)
+        silu_mul(v[i], v[i + 1], u[i], u[i + 1], v[i], v[i + 1]);
     }
   }
   // the largest magnitude's bits (a NaN or infinity is above every number)
@@ -92,7 +137,8 @@ struct Run {
   // half h's values times a power of two
   __device__ __forceinline__ void scaled(int h, float f, float (&o)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 8; i++) o[i] = __fmul_rn(v[8 * h + i], f);
+    for (int i = 0; i < 8; i += 2)
+      mul2(Two(v[8 * h + i], v[8 * h + i + 1]), Two(f)).get(o[i], o[i + 1]);
   }
 };
 
@@ -209,10 +255,14 @@ __device__ __forceinline__ uint32_t encode(const Run<F32, SWIGLU>& run, float do
 #pragma unroll
   for (int h = 0; h < 2; h++) {
     float q[8];
-    run.scaled(h, down, q);
+    run.scaled(h, F32 || SWIGLU ? -down : down, q);
 #pragma unroll
-    for (int i = 0; i < 8; i++)
-      q[i] = (F32 || SWIGLU) ? div_by(q[i], s, r) : __fmaf_rn(q[i], r, __fmul_rn(q[i], rl));
+    for (int i = 0; i < 8; i += 2) {
+      const Two x(q[i], q[i + 1]);
+      const Two y = F32 || SWIGLU ? neg_div_by(x, Two(s), Two(-r))
+                                  : fma2(x, Two(r), mul2(x, Two(rl)));
+      y.get(q[i], q[i + 1]);
+    }
     c[h] = byte == 0u ? 0u : e2m1x8(q);
   }
   return byte;
