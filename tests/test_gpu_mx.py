@@ -146,6 +146,50 @@ def test_quantize_swiglu(fmt, dtype):
     assert ok.all()
 
 
+# gates where exp(-a) nears fp32's end (at 88.72) and passes it
+FAR_GATES = [-86.0, -86.5, -86.75, -87.0, -87.25, -87.5, -88.0, -88.5, -88.7, -88.75, -89.0,
+             -95.0, -104.0, -200.0, -608.0, -1e4, -1e6, -1e30, -1e38, -3e38]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_swiglu_of_far_gates(fmt, dtype):
+    """Rows and blocks whose gates all lie around or below -87, under small and large b:
+    the bits of the documented form in fp32 (0 where exp(-a) is infinite), by
+    the quantisation and by the product that quantises its rows itself."""
+    K = 160
+    b = torch.cat([torch.logspace(-30, 38, K // 2), -torch.logspace(-30, 38, K // 2)]).float()
+    b = b[torch.arange(K) * 37 % K]  # 37 and 160 have no common factor
+    one = torch.linspace(0.5, 1.5, K)
+    rows = [(torch.full((K,), a), v) for a in FAR_GATES for v in (one, -one, b)]
+    # a block of far gates beside ordinary ones; NaN and infinities among far gates
+    mixed = torch.full((K,), -1e30)
+    mixed[32:64] = torch.linspace(-3, 3, 32)
+    rows += [(mixed, one), (mixed, b)]
+    for at, (ga, up) in enumerate([(float("nan"), 1.0), (-float("inf"), 1.0), (-1e30, float("inf")),
+                                   (-88.5, float("nan"))]):
+        a, v = torch.full((K,), -200.0), one.clone()
+        a[33 + at], v[33 + at] = ga, up
+        rows.append((a, v))
+    x = torch.stack([torch.cat(r) for r in rows]).to(dtype).cuda()
+    a, u = x.float().chunk(2, 1)
+    h = a / (1.0 + torch.exp(-a)) * u
+    q, r = bb.mx_quantize(x, fmt, swiglu=True), bb.mx_quantize(h, fmt)
+    assert torch.equal(q.codes, r.codes)
+    starts = [0, x.shape[0]]
+    assert np.array_equal(values_of(q, starts), values_of(r, starts), equal_nan=True)
+    # the rows of the largest gates are zeros, whatever b
+    last = slice(3 * FAR_GATES.index(-200.0), 3 * len(FAR_GATES))
+    assert not values_of(q, starts)[last].any()
+    W = bb.mx_quantize(synth.make_weight(130, K, 3).cuda(), fmt)
+    for i in range(0, x.shape[0], 2):
+        part = x[i:i + 2]
+        if fmt == bb.MX_E8M0:  # (bf16 and fp32 rows by the product's own kernel)
+            assert bb.mx_workspace_size(fmt, part.shape[0], K, 1, True) == 0
+        y, z = bb.mx_linear(part, W, swiglu=True), bb.mx_linear(bb.mx_quantize(h[i:i + 2], fmt), W)
+        assert torch.equal(y.isnan(), z.isnan()) and torch.equal(y.nan_to_num(7.0), z.nan_to_num(7.0))
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_quantize_gather_groups_and_strides(fmt):
     """Ragged groups (empty, one row, across tile bands), gathered rows with
