@@ -161,7 +161,8 @@ struct MxPlan {
   int pair;       // 1: two CTAs to a tile of 256 weight rows
   int ctas;
   int stages;     // 256-column stages of K
-  int64_t tiles;  // an upper bound for ragged groups
+  int64_t token_tiles;  // of all groups, and
+  int64_t tiles;        // of the output: upper bounds for ragged groups
 };
 MxPlan mx_plan(int groups, int64_t rows, int64_t N, int64_t K);
 size_t mx_scale_bytes(int fmt, int64_t rows, int64_t K, int groups);

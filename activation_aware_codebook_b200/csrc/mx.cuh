@@ -88,6 +88,19 @@ __device__ __forceinline__ void mx_group(const MxRows& g, int e, int* first, int
   }
 }
 
+// Token tiles of a group of `count` rows, and sums of them over groups, each held
+// at `most`: the plan's bound for sound offsets (at most 2^31 / 32 + 1024, so that
+// neither a sum of two nor, by the calls' checks, its product with the weight
+// tiles passes 32 bits).  Offsets that are not sound, say 0 and the last row in
+// turn, can name every row in every group; the tiles beyond the bound are left out.
+__host__ __device__ inline int mx_group_tiles(int count, int width, int most) {
+  const int tiles = count > 0 ? (count - 1) / width + 1 : 0;
+  return tiles < most ? tiles : most;
+}
+__host__ __device__ inline int mx_add_tiles(int a, int b, int most) {
+  return a + b < most ? a + b : most;
+}
+
 // Each group's scales start a tile of their own: group e, whose first row is
 // `first`, starts at band first / 128 + e.  floor(a / 128) + floor(b / 128) <=
 // floor((a + b) / 128) keeps the bands of one group clear of the next one's,

@@ -87,6 +87,7 @@ struct MxGemmArgs {
   int box;            // token rows of one TMA copy
   int bf16_out;
   int ahead;          // all but X was ready before the kernel before this one
+  int most;           // token tiles of all groups, at most
 };
 
 // Rows to quantise on the way (SRC >= 0).
@@ -368,7 +369,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   for (int e = threadIdx.x; e < a.rows.groups; e += S::kThreads) {
     int first, last;
     mx_group(a.rows, e, &first, &last);
-    s_pre[e + 1] = (last - first + a.width - 1) / a.width;
+    s_pre[e + 1] = mx_group_tiles(last - first, a.width, a.most);
   }
   tc_fence_before();
   __syncthreads();
@@ -379,10 +380,11 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       int v = e0 + lane < a.rows.groups ? s_pre[e0 + lane + 1] : 0;
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
+        if (lane >= o) v = mx_add_tiles(u, v, a.most);
       }
-      if (e0 + lane < a.rows.groups) s_pre[e0 + lane + 1] = sum + v;
-      sum += __shfl_sync(0xffffffffu, v, 31);
+      v = mx_add_tiles(sum, v, a.most);
+      if (e0 + lane < a.rows.groups) s_pre[e0 + lane + 1] = v;
+      sum = __shfl_sync(0xffffffffu, v, 31);
     }
   }
   if (a.rows.groups > 1) __syncthreads();
@@ -1014,7 +1016,8 @@ MxPlan mx_plan(int groups, int64_t rows, int64_t N, int64_t K) {
   p.nt = p.width > 128 ? 256 : p.width;
   const int64_t n = p.pair ? n2 : n1;
   // an upper bound of the tiles: sum ceil(c / width) <= rows / width + one per busy group
-  p.tiles = groups == 1 ? (rows + p.width - 1) / p.width * n : (rows / p.width + busy) * n;
+  p.token_tiles = groups == 1 ? (rows + p.width - 1) / p.width : rows / p.width + busy;
+  p.tiles = p.token_tiles * n;
   if (p.tiles > 65535) p.split = 1;  // a grid's y
   p.stages = (int)stages;
   p.ctas = p.pair ? kSms : (int)(p.split > 1 ? p.tiles * p.split : (p.tiles < kSms ? p.tiles : kSms));
@@ -1053,7 +1056,7 @@ cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f
   const MxGemmArgs a{x.row_scale, w.row_scale, Y, ldy,
                      MxRows{x.offsets, x.groups, (int)x.rows}, (int)N, (int)x.K,
                      (int)((N + kWRows - 1) / kWRows + p.pair) / (1 + p.pair), p.stages, p.width, box,
-                     f32 ? 0 : 1, overlap ? 1 : 0};
+                     f32 ? 0 : 1, overlap ? 1 : 0, (int)p.token_tiles};
   if (src) {
     int warps = 1;
     while (2 * warps < (int)x.rows) warps *= 2;

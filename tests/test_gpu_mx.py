@@ -579,6 +579,25 @@ def test_offsets_that_are_not_sound_stay_inside():
     assert bb.device_timeouts() == 0
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_offsets_that_name_every_row_in_every_group(fmt):
+    """1024 groups, every other one of all rows: the tiles beyond the plan's
+    bound are left out, nothing around the output is touched, and the call after
+    it is right."""
+    E, N, K, R = 1024, 40, 96, 3000
+    W = bb.mx_quantize(synth.make_weight(E * N, K, 4).cuda(), fmt, groups=E)
+    x = activations(R, K, 3).cuda()
+    wild = torch.tensor([0, R] * (E // 2) + [0], dtype=torch.int32).cuda()
+    whole = torch.full((R + 2, N), 6.0, device="cuda")
+    bb.mx_linear(x, W, out=whole[1:-1], offsets=wild)
+    torch.cuda.synchronize()
+    assert (whole[[0, -1]] == 6.0).all() and bb.device_timeouts() == 0
+    sound = [0] * 512 + [R] * 513
+    off = torch.tensor(sound, dtype=torch.int32).cuda()
+    X = bb.mx_quantize(x, fmt, groups=E, offsets=off)
+    check_product(bb.mx_linear(X, W), X, W, sound, E)
+
+
 def test_binding_refusals():
     x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
     W = bb.mx_quantize(x, bb.MX_E4M3)

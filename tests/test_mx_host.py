@@ -1,6 +1,7 @@
 """Host-side checks of the microscaled calls (no GPU): sizes, plans, and the
 refusals, which all come before anything is launched."""
 import ctypes
+import subprocess
 
 import numpy as np
 import pytest
@@ -182,6 +183,60 @@ def test_plan_covers_every_split_of_the_rows(lib, groups, rows, N, K):
         assert tiles <= p["tiles"]
     if p["split"] > 1:  # a cluster a tile, within a grid's limits
         assert p["ctas"] == p["tiles"] * p["split"] and p["tiles"] <= 65535
+
+
+_TILES = r"""
+#include <cstdio>
+#include "mx.cuh"
+// lines of: width most groups offsets[groups + 1] -> the running sums of the tiles
+int main() {
+  int width, most, groups, rows;
+  while (scanf("%d %d %d %d", &width, &most, &groups, &rows) == 4) {
+    (void)rows;
+    int sum = 0, from, to;
+    if (scanf("%d", &from) != 1) return 1;
+    for (int e = 0; e < groups; e++, from = to) {
+      if (scanf("%d", &to) != 1) return 1;
+      const int last = to < from ? from : to;  // as the kernels read a group
+      sum = aaac::mx_add_tiles(sum, aaac::mx_group_tiles(last - from, width, most), most);
+      printf("%d ", sum);
+    }
+    printf("\n");
+  }
+}
+"""
+
+
+def test_tile_sums_hold_for_any_offsets(lib, tmp_path):
+    """The kernel's tile counts on the host: exact for sound offsets, and for
+    descending ones inside the plan's bound, whose product with the weight tiles
+    stays inside 32 bits (512 groups of 2^24 rows alone make 2^26 tiles of 128
+    rows, 2^32 with 64 weight tiles); a group of 2^31 - 1 rows is counted whole."""
+    (tmp_path / "tiles.cu").write_text(_TILES)
+    subprocess.run([cbuild.NVCC, "-std=c++17", *cbuild.ARCH, "-I", cbuild.HERE, "-o",
+                    str(tmp_path / "tiles"), str(tmp_path / "tiles.cu")], check=True)
+    cases, text = [], ""
+    r = np.random.RandomState(7)
+    for groups, rows, N in ((1, (1 << 31) - 1, 1), (1024, 1 << 24, 8192), (1024, 17000000, 8192),
+                            (1024, 300, 150), (6, 2620, 2600), (33, 70000, 1000)):
+        p = bb.mx_launch_plan(groups, rows, N, 64)
+        n_tiles = -(-N // p["rows"])
+        most = p["tiles"] // n_tiles
+        assert p["tiles"] == most * n_tiles < 1 << 31
+        sound = np.concatenate([[0], np.sort(r.randint(0, rows, groups - 1)), [rows]])
+        wild = np.where(np.arange(groups + 1) % 2, rows, 0)
+        for offsets in (sound, wild, sound[::-1]):
+            cases.append((p["columns"], most, rows, offsets.tolist(), offsets is sound))
+            text += f"{p['columns']} {most} {groups} {rows} " + " ".join(map(str, offsets)) + "\n"
+    out = subprocess.run([str(tmp_path / "tiles")], input=text, capture_output=True, text=True,
+                         check=True).stdout.splitlines()
+    assert len(out) == len(cases)
+    for line, (width, most, rows, offsets, sound) in zip(out, cases):
+        got = list(map(int, line.split()))
+        exact = np.cumsum([max(-(-(b - a) // width), 0) for a, b in zip(offsets, offsets[1:])])
+        assert got == np.minimum(exact, most).tolist()
+        if sound:
+            assert got == exact.tolist()
 
 
 def test_plan_refusals(lib):
