@@ -192,7 +192,8 @@ def device_checks() -> int:
 
 def inject_fault(kind: Optional[str]) -> None:
     """Test hook: the next call that would launch work fails on the host
-    ("alloc", "launch" or "sync"; None disarms); see aaac_inject_fault."""
+    ("alloc", "launch" or "sync"; None disarms), or, in checked builds, the
+    products' device waits run out ("wait"); see aaac_inject_fault."""
     _check(load().aaac_inject_fault(None if kind is None else kind.encode()))
 
 

@@ -852,12 +852,32 @@ int aaac_checked_build(void) {
 #endif
 }
 
+#ifdef AAAC_CHECKS
+static aaac_status set_patience(int tiles) {
+  return from_cuda(aaac::mx_set_patience(tiles), "aaac_inject_fault");
+}
+#endif
+
 aaac_status aaac_inject_fault(const char* kind) {
+  static std::atomic<bool> waits_armed{false};
+  if (kind && !strcmp(kind, "wait")) {
+#ifdef AAAC_CHECKS
+    waits_armed.store(true);
+    return set_patience(1);
+#else
+    return fail(AAAC_ERR_UNSUPPORTED, "fault kind 'wait' needs a checked build");
+#endif
+  }
   const int k = fault_kind(kind);
   if (k < 0)
-    return fail(AAAC_ERR_INVALID_ARG, "unknown fault kind '%s' (alloc, launch, sync or empty)",
-                kind);
+    return fail(AAAC_ERR_INVALID_ARG,
+                "unknown fault kind '%s' (alloc, launch, sync, wait or empty)", kind);
   g_fault.store(k);
+#ifdef AAAC_CHECKS
+  if (k == kFaultNone && waits_armed.exchange(false)) return set_patience(INT32_MAX);
+#else
+  (void)waits_armed;
+#endif
   return ok();
 }
 

@@ -177,5 +177,8 @@ bool mx_own_rows(int fmt, int groups, int64_t rows, int64_t K, bool swiglu);
 cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f32, int64_t ldy,
                            const MxSource* src, bool overlap, cudaStream_t st);
 cudaError_t mx_timeout_flag(unsigned int* out);
+#ifdef AAAC_CHECKS
+cudaError_t mx_set_patience(int tiles);  // see g_patience
+#endif
 
 }  // namespace aaac

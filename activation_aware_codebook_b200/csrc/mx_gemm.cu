@@ -51,7 +51,8 @@
 // decoding): eight more warps quantise each stage's columns straight into its
 // shared memory, as mx_quant.cu would, while the weights stream in: one
 // launch, and no workspace.
-// Waits are bounded (tcgen05.cuh); a CTA that gives up writes NaN.
+// Waits are bounded (tcgen05.cuh); a CTA that gives up writes NaN to the rest of
+// its tiles.
 #include <math.h>
 
 #include "common.cuh"
@@ -669,6 +670,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     float* gx = s_gx[warp - kEpiWarp];           // the row scales of its tokens
     TileAt t;
     int e = 0, i = 0;
+    bool fail = false;  // a wait ran out: NaN for this tile and all that follow
     for (int item = item0; item < items; item += step, i++) {
       tile_at<S::kTileRows>(a, s_pre, item, &e, &t);
       const int b = i % TM::kBufs;
@@ -687,14 +689,14 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
           __syncwarp();
         }
       }
-      const bool got = __all_sync(0xffffffffu, mbar_wait(&acc_full[b], (i / TM::kBufs) & 1));
+      if (!fail) fail = !epilogue_wait(&acc_full[b], (i / TM::kBufs) & 1, i);
+      fail = __any_sync(0xffffffffu, fail || s_fail);
       tc_fence_after();
       if (FMT == kMxE4m3 && !SPLIT && S::kOwn) {  // written before the last stage was
         __syncwarp();
         if (lane < NC) gx[lane] = lane < mine ? s_scale[part * NC + lane] : 0.0f;
         __syncwarp();
       }
-      const bool fail = !got || s_fail;
       const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NT + part * NC);
       if (SPLIT) {
         // every MMA of this CTA is complete, so the stages are free
@@ -719,7 +721,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
           if (a.bf16_out) *reinterpret_cast<__nv_bfloat16*>(y) = __float2bfloat16_rn(__int_as_float(0x7fc00000));
           else *reinterpret_cast<float*>(y) = __int_as_float(0x7fc00000);
         }
-        break;  // the MMA warp stopped; nothing more to read
+        continue;
       }
       auto take = [&](int c0, uint32_t (&r)[CH]) {
 #pragma unroll
@@ -1070,5 +1072,9 @@ cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f
 cudaError_t mx_timeout_flag(unsigned int* out) {
   return cudaMemcpyFromSymbol(out, g_wait_timeout, sizeof(unsigned int));
 }
+
+#ifdef AAAC_CHECKS
+cudaError_t mx_set_patience(int tiles) { return cudaMemcpyToSymbol(g_patience, &tiles, sizeof(int)); }
+#endif
 
 }  // namespace aaac

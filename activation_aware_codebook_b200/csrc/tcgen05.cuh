@@ -70,6 +70,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// Checked builds (common.cuh): the tiles for which an epilogue waits; from then
+// on its waits count as run out (aaac_inject_fault("wait")).  Like the flag, one
+// per translation unit.
+#ifdef AAAC_CHECKS
+__device__ int g_patience = 0x7fffffff;
+#endif
+
+// An epilogue's wait, by the whole warp, for the accumulator of the CTA's tile
+// number `tile`.
+__device__ __forceinline__ bool epilogue_wait(uint64_t* bar, uint32_t parity, int tile) {
+#ifdef AAAC_CHECKS
+  if (tile >= *(volatile int*)&g_patience) {
+    atomicExch(&g_wait_timeout, 1u);
+    return false;
+  }
+#endif
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int x, int y) {
   asm volatile(

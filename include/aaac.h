@@ -471,6 +471,11 @@ aaac_status aaac_device_checks(uint32_t* flag);
  * disarms the fault.  The environment variable AAAC_FAULT with the same
  * kinds arms one fault when the library first runs a call.  For testing a
  * caller's error paths; nothing reaches the GPU.
+ * Kind "wait", in checked builds only (AAAC_ERR_UNSUPPORTED elsewhere): until
+ * NULL or "" disarms it, the epilogues of aaac_mx_linear's kernels give up
+ * after a CTA's first tile as though their bounded wait had run out (the other
+ * waits of the kernel then do run out, after about 2 seconds).  It writes a
+ * device variable.
  * Errors: AAAC_ERR_INVALID_ARG for an unknown kind. */
 aaac_status aaac_inject_fault(const char* kind);
 

@@ -67,3 +67,61 @@ def test_checked_build_runs_clean_and_agrees(tmp_path):
     a = torch.load(tmp_path / "checked.pt")
     b = torch.load(tmp_path / "plain.pt")
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+_WAIT_CHILD = r"""
+import sys, torch
+from activation_aware_codebook_b200 import binding as bb, synth
+assert bb.load().aaac_checked_build() == 1, "not the checked build"
+dev = "cuda"
+# rows, N, K, groups: persistent CTAs, pairs of CTAs, ragged groups; four tiles a CTA or more
+cases = [(100, 128 * 600 + 5, 288, 1, 128), (1100, 128 * 120, 288, 1, 256),
+         (130, 128 * 60 + 5, 288, 8, 128)]
+for fmt in (bb.MX_E8M0, bb.MX_E4M3):
+    for M, N, K, E, rows in cases:
+        p = bb.mx_launch_plan(E, M, N, K)
+        assert p["rows"] == rows and p["split"] == 1 and p["tiles"] * rows >= 4 * 148 * 128, p
+        off = (None if E == 1 else
+               torch.arange(E + 1, dtype=torch.int32, device=dev) * (M // E) + 2)
+        X = bb.mx_quantize(synth.make_activations(M, K, M, True, device=dev), fmt, groups=E, offsets=off)
+        W = bb.mx_quantize(synth.make_weight(E * N, K, 3, device=dev), fmt, groups=E)
+        want = torch.full((M, N), 3.0, device=dev)
+        bb.mx_linear(X, W, out=want)
+        assert torch.isfinite(want).all()
+        got = torch.full((M, N), 5.0, device=dev)
+        bb.inject_fault("wait")
+        bb.mx_linear(X, W, out=got)
+        torch.cuda.synchronize()
+        bb.inject_fault(None)
+        nan = got.isnan()
+        inside = slice(0, M) if E == 1 else slice(2, int(off[-1]))
+        rest = torch.ones(M, dtype=torch.bool, device=dev)
+        rest[inside] = False
+        assert (got[rest] == 5.0).all()
+        # every tile was written: the first ones of each CTA, and NaN
+        print("CASE", fmt, M, N, E, int(nan.sum()), int((got[inside] == 5.0).sum()),
+              bool((nan | (got == want))[inside].all()))
+        assert 0 < int(nan.sum()) < nan.numel()
+        assert (nan | (got == want))[inside].all(), "tiles keep what was there"
+        bb.mx_linear(X, W, out=got)
+        assert torch.equal(got[inside], want[inside])
+assert bb.device_timeouts() == 1
+print("WAITS OK")
+"""
+
+
+@pytest.mark.gpu
+def test_a_product_whose_wait_runs_out_writes_nan_everywhere():
+    """The epilogue gives up after a CTA's first tile: every later tile of the
+    CTA is NaN, not what the buffer held; the status says so, and the next
+    product on the same context is right."""
+    cbuild.build(checks=True)
+    env = dict(os.environ, AAAC_CHECKED="1", PYTHONPATH=ROOT)
+    res = subprocess.run([sys.executable, "-c", _WAIT_CHILD], env=env, cwd=ROOT,
+                         capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and "WAITS OK" in res.stdout, res.stdout + res.stderr[-3000:]
+
+
+def test_waits_run_out_in_checked_builds_only():
+    cbuild.build()
+    assert bb.load().aaac_inject_fault(b"wait") == 4  # AAAC_ERR_UNSUPPORTED
