@@ -853,16 +853,18 @@ int aaac_checked_build(void) {
 }
 
 #ifdef AAAC_CHECKS
+static std::atomic<bool> g_waits_armed{false};
 static aaac_status set_patience(int tiles) {
-  return from_cuda(aaac::mx_set_patience(tiles), "aaac_inject_fault");
+  cudaError_t e = aaac::mx_set_patience(tiles);
+  if (e == cudaSuccess) e = aaac::gemm_set_patience(tiles);
+  return from_cuda(e, "aaac_inject_fault");
 }
 #endif
 
 aaac_status aaac_inject_fault(const char* kind) {
-  static std::atomic<bool> waits_armed{false};
   if (kind && !strcmp(kind, "wait")) {
 #ifdef AAAC_CHECKS
-    waits_armed.store(true);
+    g_waits_armed.store(true);
     return set_patience(1);
 #else
     return fail(AAAC_ERR_UNSUPPORTED, "fault kind 'wait' needs a checked build");
@@ -874,9 +876,7 @@ aaac_status aaac_inject_fault(const char* kind) {
                 "unknown fault kind '%s' (alloc, launch, sync, wait or empty)", kind);
   g_fault.store(k);
 #ifdef AAAC_CHECKS
-  if (k == kFaultNone && waits_armed.exchange(false)) return set_patience(INT32_MAX);
-#else
-  (void)waits_armed;
+  if (k == kFaultNone && g_waits_armed.exchange(false)) return set_patience(INT32_MAX);
 #endif
   return ok();
 }

@@ -34,8 +34,8 @@
 // both halves add their partial tiles with float atomics (two terms onto
 // zero: the result does not depend on their order).
 // Every mbarrier wait is bounded by the global timer (about 2 s); a wait that
-// runs out sets a device flag, the tile is written as NaN and the CTA still
-// releases its TMEM.
+// runs out sets a device flag, the tile (and what tiles the CTA has left) is
+// written as NaN, and the CTA still releases its TMEM.
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
@@ -450,12 +450,13 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
     const int q = warp & 3;               // TMEM lane quadrant this warp may read
     const int half = (warp - 2) >> 2;     // which half of the token columns
     int i = 0;
+    bool fail = false;  // a wait ran out: NaN for this tile and all that follow
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, i++) {
       const int b = i & 1;
       const int n0 = (tile / tiles_t) * kBN, t0 = (tile % tiles_t) * kBTT;
-      const bool got = __all_sync(0xffffffffu, mbar_wait(&acc_full[b], (i >> 1) & 1));
+      if (!fail) fail = !epilogue_wait(&acc_full[b], (i >> 1) & 1, i);
+      fail = __any_sync(0xffffffffu, fail || s_fail);
       tc_fence_after();
-      const bool fail = !got || s_fail;
       const int nrow = n0 + q * 32 + lane;
       for (int j0 = half * (kBTT / 2); j0 < (half + 1) * (kBTT / 2); j0 += 32) {
         uint32_t r[32];
@@ -467,7 +468,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
             a.Y[(int64_t)t * a.N + nrow] = fail ? __int_as_float(0x7fc00000) : __uint_as_float(r[j]);
         }
       }
-      if (fail) break;  // the MMA warp stopped; nothing more to read
+      if (fail) continue;  // nothing more to read
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[b]);
@@ -996,5 +997,11 @@ cudaError_t launch_gemm_dequantised(const uint16_t* X, int64_t M, int64_t ldx,
 cudaError_t gemm_timeout_flag(unsigned int* out) {
   return cudaMemcpyFromSymbol(out, g_wait_timeout, sizeof(unsigned int));
 }
+
+#ifdef AAAC_CHECKS
+cudaError_t gemm_set_patience(int tiles) {
+  return cudaMemcpyToSymbol(g_patience, &tiles, sizeof(int));
+}
+#endif
 
 }  // namespace aaac

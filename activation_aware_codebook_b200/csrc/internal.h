@@ -179,6 +179,7 @@ cudaError_t launch_mx_gemm(const MxTensor& x, const MxTensor& w, void* Y, bool f
 cudaError_t mx_timeout_flag(unsigned int* out);
 #ifdef AAAC_CHECKS
 cudaError_t mx_set_patience(int tiles);  // see g_patience
+cudaError_t gemm_set_patience(int tiles);
 #endif
 
 }  // namespace aaac

@@ -450,8 +450,8 @@ aaac_status aaac_mx_launch_plan(int32_t groups, int64_t rows, int64_t N, int64_t
 /* Device-side wait status of the current device: *flag = 1 when a bounded
  * wait inside one of the library's kernels (the tensor-core paths of aaac_linear
  * and aaac_mx_linear) has run out since the library was loaded, else 0.  A
- * kernel whose wait ran out writes NaN to its output tile and still releases
- * its tensor memory.  Synchronises with the device (reads a device variable). */
+ * CTA whose wait ran out writes NaN to the output tiles that it has not
+ * finished and still releases its tensor memory.  Synchronises with the device (reads a device variable). */
 aaac_status aaac_device_timeouts(uint32_t* flag);
 
 /* Debug builds: 1 when the library was compiled with AAAC_CHECKS
@@ -472,9 +472,10 @@ aaac_status aaac_device_checks(uint32_t* flag);
  * kinds arms one fault when the library first runs a call.  For testing a
  * caller's error paths; nothing reaches the GPU.
  * Kind "wait", in checked builds only (AAAC_ERR_UNSUPPORTED elsewhere): until
- * NULL or "" disarms it, the epilogues of aaac_mx_linear's kernels give up
- * after a CTA's first tile as though their bounded wait had run out (the other
- * waits of the kernel then do run out, after about 2 seconds).  It writes a
+ * NULL or "" disarms it, the epilogues of the persistent tensor-core kernels
+ * (aaac_linear_ws, aaac_mx_linear) give up after a CTA's first tile as though
+ * their bounded wait had run out (the other waits of the kernel then do run
+ * out, after about 2 seconds).  It writes a
  * device variable.
  * Errors: AAAC_ERR_INVALID_ARG for an unknown kind. */
 aaac_status aaac_inject_fault(const char* kind);

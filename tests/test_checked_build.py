@@ -109,16 +109,44 @@ assert bb.device_timeouts() == 1
 print("WAITS OK")
 """
 
+_WAIT_LINEAR_CHILD = r"""
+import torch
+from activation_aware_codebook_b200 import binding as bb, synth
+assert bb.load().aaac_checked_build() == 1, "not the checked build"
+M, N, K = 1100, 128 * 120 + 5, 256  # 605 tiles of 128 x 256: four a CTA
+cfg = bb.Config(bb.INT4, 128, 16, 1)
+packed = bb.run_layer(synth.make_weight(N, K, 3, device="cuda"),
+                      synth.make_activations(64, K, 4, True, device="cuda"), cfg)
+x = synth.make_activations(M, K, 5, True, device="cuda")
+ws = torch.empty(bb.linear_workspace_size(cfg, M, N, K), dtype=torch.uint8, device="cuda")
+assert ws.numel() > 0
+want = bb.linear(x, packed, cfg, N, K, ws=ws)
+assert torch.isfinite(want).all()
+got = torch.full((M, N), 5.0, device="cuda")
+bb.inject_fault("wait")
+bb.linear(x, packed, cfg, N, K, ws=ws, out=got)
+torch.cuda.synchronize()
+bb.inject_fault(None)
+nan = got.isnan()
+print("CASE", int(nan.sum()), int((got == 5.0).sum()), nan.numel())
+assert 0 < int(nan.sum()) < nan.numel()
+assert (nan | (got == want)).all(), "tiles keep what was there"
+assert bb.device_timeouts() == 1
+assert torch.equal(bb.linear(x, packed, cfg, N, K, ws=ws), want)
+print("WAITS OK")
+"""
+
 
 @pytest.mark.gpu
-def test_a_product_whose_wait_runs_out_writes_nan_everywhere():
+@pytest.mark.parametrize("child", [_WAIT_CHILD, _WAIT_LINEAR_CHILD], ids=["mx_linear", "linear"])
+def test_a_product_whose_wait_runs_out_writes_nan_everywhere(child):
     """The epilogue gives up after a CTA's first tile: every later tile of the
     CTA is NaN, not what the buffer held; the status says so, and the next
     product on the same context is right."""
     cbuild.build(checks=True)
     env = dict(os.environ, AAAC_CHECKED="1", PYTHONPATH=ROOT)
-    res = subprocess.run([sys.executable, "-c", _WAIT_CHILD], env=env, cwd=ROOT,
-                         capture_output=True, text=True, timeout=300)
+    res = subprocess.run([sys.executable, "-c", child], env=env, cwd=ROOT, capture_output=True,
+                         text=True, timeout=300)
     assert res.returncode == 0 and "WAITS OK" in res.stdout, res.stdout + res.stderr[-3000:]
 
 
