@@ -445,6 +445,9 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
         if (!ok) { s_fail = 1; break; }
         mma_commit(&acc_full[b]);
       }
+      // the MMAs are complete before tensor memory is given back (bounded): an
+      // epilogue that gave up has not waited for them
+      if (it > 0 && !mbar_wait(&empty[(it - 1) % kStagesT], ((it - 1) / kStagesT) & 1)) s_fail = 1;
     }
   } else {
     const int q = warp & 3;               // TMEM lane quadrant this warp may read

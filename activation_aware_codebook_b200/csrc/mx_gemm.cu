@@ -281,6 +281,14 @@ struct Ring {
   }
 };
 
+// The use before the ring's own, of the stage before, is over; at once where
+// there was none (a new barrier's phase before its first is complete).
+template <int STAGES>
+__device__ __forceinline__ void wait_last(uint64_t* bars, const Ring<STAGES>& ring) {
+  const bool back = ring.s == 0;
+  warp_wait(&bars[back ? STAGES - 1 : ring.s - 1], ring.phase ^ (back ? 1u : 0u));
+}
+
 // The tensor core's N for `count` tokens; a pair's CTAs hold half of it each.
 template <bool TWO>
 __device__ __forceinline__ int mma_n(int count) {
@@ -407,6 +415,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   const int nst = st_hi - st_lo;
   const int items = s_pre[a.rows.groups] * a.n_tiles;
 
+  Ring<S::kStages> mma_ring;  // warp 1's walk
   if (warp == 0) {
     const bool one = elect_one();
     // coordinates of a tile's copies: the rows of the codes and the bands of
@@ -469,10 +478,12 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       }
       if (SPLIT) break;
     }
-    // the last copies have landed before the CTA can exit (bounded)
-    for (int j = it > S::kStages ? it - S::kStages : 0; j < it && ok; j++)
-      ok = warp_wait(&full[j % S::kStages], (j / S::kStages) & 1);
-    if (!ok) s_fail = 1;
+    // the last copies have landed before the CTA can exit (bounded), also where
+    // it gives up
+    bool landed = true;
+    for (int j = it > S::kStages ? it - S::kStages : 0; j < it && landed; j++)
+      landed = warp_wait(&full[j % S::kStages], (j / S::kStages) & 1);
+    if (!ok || !landed) s_fail = 1;
   } else if (warp == 1) {
     if (!TWO || crank == 0) {
       const bool one = elect_one();
@@ -480,7 +491,6 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       // addresses in 16-byte units, as descriptors hold them
       const uint32_t w_lo = smem_u32(sW) >> 4, x_lo = smem_u32(sX) >> 4;
       TileAt t;
-      Ring<S::kStages> ring;
       int e = 0, i = 0;
       bool ok = true;
       for (int item = item0; item < items && ok; item += step, i++) {
@@ -496,14 +506,14 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         // are only used where there is a single one (mx_plan).
         const uint32_t shift = (uint32_t)(t.local % 128) / 32;
         const uint32_t idesc = mx_idesc<FMT>(S::kTileRows, mma_n<TWO>(t.count));
-        for (int st = st_lo; st < st_hi; st++, ring.next()) {
+        for (int st = st_lo; st < st_hi; st++, mma_ring.next()) {
           // the scale warps arrive after the whole stage has landed
-          ok = warp_wait(&scale_full[ring.s], ring.phase);
+          ok = warp_wait(&scale_full[mma_ring.s], mma_ring.phase);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sc = tmem + TM::kScale + ring.s * (TM::kScaleX + 16);
-          const uint32_t w0 = w_lo + ring.s * (kWTile >> 4);
-          const uint32_t x0 = x_lo + ring.s * (S::kXTile >> 4);
+          const uint32_t sc = tmem + TM::kScale + mma_ring.s * (TM::kScaleX + 16);
+          const uint32_t w0 = w_lo + mma_ring.s * (kWTile >> 4);
+          const uint32_t x0 = x_lo + mma_ring.s * (S::kXTile >> 4);
           const int steps = min(kSteps, steps_all - st * kSteps);
           if (one) {
 #pragma unroll
@@ -516,7 +526,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                                  sc + TM::kScaleX + 4 * atom, sc + 4 * S::kSub * atom + shift,
                                  (st > st_lo || k > 0) ? 1u : 0u);
               }
-            commit_mx<TWO>(&empty[ring.s]);
+            commit_mx<TWO>(&empty[mma_ring.s]);
           }
           __syncwarp();
         }
@@ -691,6 +701,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       }
       if (!fail) fail = !epilogue_wait(&acc_full[b], (i / TM::kBufs) & 1, i);
       fail = __any_sync(0xffffffffu, fail || s_fail);
+      if (fail) s_fail = 1;
       tc_fence_after();
       if (FMT == kMxE4m3 && !SPLIT && S::kOwn) {  // written before the last stage was
         __syncwarp();
@@ -788,8 +799,15 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     }
   }
   tc_fence_before();
-  if (TWO) cluster_sync_all();  // neither CTA's memory is in use by the other
-  else __syncthreads();
+  // The MMAs are complete before tensor memory is given back (bounded): where
+  // the epilogue gave up, it has not waited for them.
+  if (TWO) {
+    if (warp == 1) wait_last(empty, mma_ring);
+    cluster_sync_all();  // neither CTA's memory is in use by the other
+  } else {
+    __syncthreads();
+    if (warp == 1 && s_fail) wait_last(empty, mma_ring);
+  }
   if (warp == 1) {
     tc_fence_after();
     if (TWO)
