@@ -301,6 +301,30 @@ def test_linear_tokens(fmt, M, out_dtype):
         assert torch.equal(bb.mx_linear(x.cuda(), W, out_dtype=out_dtype), Y)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 200, 4096), (8, 200, 512), (17, 200, 2080), (160, 130, 288),
+                                   (100, 128 * 150, 96), (520, 128 * 80, 96)])
+@pytest.mark.parametrize("x_top,w_top", [(3e38, 1e-30), (1e-30, 3e38), (1e31, 1e-10), (1e-37, 1e36),
+                                         (1e-36, 1e-3), (1e-20, 1e-22), (1e18, 1e18)])
+def test_linear_range_of_row_scales(M, N, K, x_top, w_top):
+    """E4M3 row scales far from 1: where the product is in range, so is Y, by
+    split, walking and paired CTAs and by the product's own quantisation.
+    Row scales are powers of two, exact beside the sum but for subnormal Y
+    (half a step of 2^-149 for each of two roundings)."""
+    g = torch.Generator().manual_seed(K)
+    x = (torch.rand(M, K, generator=g) * 2 - 1) * x_top
+    w = (torch.rand(N, K, generator=g) * 2 - 1) * w_top
+    X, W = bb.mx_quantize(x.cuda(), bb.MX_E4M3), bb.mx_quantize(w.cuda(), bb.MX_E4M3)
+    xv, wv = values_of(X, [0, M]), values_of(W, [0, N])
+    ref = xv @ wv.T
+    bound = (K / 64 + 8) * 2.0 ** -23 * (np.abs(xv) @ np.abs(wv).T) + 2.0 ** -149
+    for Y in (bb.mx_linear(X, W), bb.mx_linear(x.cuda(), W)):
+        assert torch.isfinite(Y).all()
+        assert (np.abs(f64(Y) - ref) <= bound).all()
+    # a row of zeros stays one beside the largest scales
+    x[0] = 0.0
+    assert not bb.mx_linear(x.cuda(), W)[0].any()
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_linear_many_tiles(fmt):
     """More tiles than SMs: persistent CTAs over several tiles, an accumulator reused."""
