@@ -674,6 +674,8 @@ def _mx_source(X: torch.Tensor, rows: Optional[torch.Tensor], swiglu: bool):
     if kind is None or X.dim() != 2:
         raise ValueError("X must be a bfloat16 or float32 matrix")
     n, width = X.shape
+    if swiglu and width % 2:
+        raise ValueError(f"X has {width} columns, not two halves")
     ldx, step = X.stride()
     at = X.data_ptr()
     # 16-byte aligned rows: 8 bf16 or 4 fp32 values

@@ -2,6 +2,7 @@
 refusals, which all come before anything is launched."""
 import ctypes
 import subprocess
+import types
 
 import numpy as np
 import pytest
@@ -253,3 +254,13 @@ def test_binding_refuses_without_cuda(lib):
         pytest.skip("a GPU is present")
     with pytest.raises(RuntimeError):
         bb.mx_quantize(torch.zeros(8, 64, dtype=torch.bfloat16), bb.MX_E4M3)
+
+
+def test_swiglu_needs_two_halves():
+    """An odd width has no halves: 65 columns of a padded buffer are not 2 x 32."""
+    import torch
+    x = torch.zeros(4, 72, dtype=torch.bfloat16)[:, :65]
+    with pytest.raises(ValueError, match="halves"):
+        bb.mx_quantize(x, bb.MX_E4M3, swiglu=True)
+    with pytest.raises(ValueError, match="halves"):
+        bb.mx_linear(x, types.SimpleNamespace(K=32), swiglu=True)
