@@ -696,7 +696,10 @@ def _mx_source(X: torch.Tensor, rows: Optional[torch.Tensor], swiglu: bool):
 def _mx_out(out: Optional[torch.Tensor], rows: int, cols: int, dtype, device):
     """(output, its aaac_type, its leading dimension)."""
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device), _MX_TYPES[dtype], cols
+        kind = _MX_TYPES.get(dtype)
+        if kind is None:
+            raise ValueError(f"the output is bfloat16 or float32, not {dtype}")
+        return torch.empty((rows, cols), dtype=dtype, device=device), kind, cols
     if (out.shape != (rows, cols) or out.dtype not in _MX_TYPES
             or (cols > 1 and out.stride(1) != 1)):
         raise ValueError(f"out must be a bfloat16 or float32 [{rows}, {cols}] with "

@@ -264,3 +264,12 @@ def test_swiglu_needs_two_halves():
         bb.mx_quantize(x, bb.MX_E4M3, swiglu=True)
     with pytest.raises(ValueError, match="halves"):
         bb.mx_linear(x, types.SimpleNamespace(K=32), swiglu=True)
+
+
+def test_output_types_are_refused_by_name():
+    import torch
+    for dtype in (torch.float16, torch.float64, torch.int32):
+        with pytest.raises(ValueError, match="bfloat16 or float32"):
+            bb._mx_out(None, 4, 4, dtype, "cpu")
+    y, kind, ld = bb._mx_out(None, 4, 5, torch.bfloat16, "cpu")
+    assert y.shape == (4, 5) and y.dtype == torch.bfloat16 and (kind, ld) == (0, 5)
