@@ -793,6 +793,8 @@ def _mx_linear(X, W, out, out_dtype, rows, swiglu, offsets, ws, stream):
     device = X.get_device()
     if K != W.K:
         raise ValueError(f"X has K={K}, W has K={W.K}")
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
     _mx_on(device, rows, offsets, out, ws)
     _mx_same(device, W)
     if offsets is not None:

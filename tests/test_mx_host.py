@@ -273,3 +273,13 @@ def test_output_types_are_refused_by_name():
             bb._mx_out(None, 4, 4, dtype, "cpu")
     y, kind, ld = bb._mx_out(None, 4, 5, torch.bfloat16, "cpu")
     assert y.shape == (4, 5) and y.dtype == torch.bfloat16 and (kind, ld) == (0, 5)
+
+
+def test_workspace_of_fewer_bytes_than_elements_is_refused():
+    """numel() of an expanded or strided tensor says nothing about its bytes."""
+    import torch
+    x, W = torch.zeros(40, 64, dtype=torch.bfloat16), types.SimpleNamespace(K=64)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20),
+               torch.zeros(1 << 20, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            bb.mx_linear(x, W, ws=ws)
