@@ -732,7 +732,6 @@ aaac_status aaac_mx_quantize(const aaac_mx_source* src, const aaac_mx_tensor* q,
   CHECK(check_mx_source(src, q->rows, q->K));
   CHECK(take_fault());
   if (q->rows == 0) return ok();
-  aaac::count_launches(1);
   return from_cuda(aaac::launch_mx_quantize(mx_source_of(src), mx_of(q), (cudaStream_t)stream),
                    "aaac_mx_quantize");
 }
@@ -744,7 +743,6 @@ aaac_status aaac_mx_dequant(const aaac_mx_tensor* q, void* out, int32_t type, in
   CHECK(check_mx_out(out, type, ldo, q->K, q->rows, 16));
   CHECK(take_fault());
   if (q->rows == 0) return ok();
-  aaac::count_launches(1);
   return from_cuda(
       aaac::launch_mx_dequant(mx_of(q), out, type == AAAC_F32, ldo, (cudaStream_t)stream),
       "aaac_mx_dequant");
@@ -758,7 +756,6 @@ aaac_status aaac_mx_linear(const aaac_mx_tensor* x, const aaac_mx_tensor* w, voi
   CHECK(check_mx_out(Y, type, ldy, w->rows / w->groups, x->rows, 1));
   CHECK(take_fault());
   if (x->rows == 0) return ok();
-  aaac::count_launches(1);
   return from_cuda(aaac::launch_mx_gemm(mx_of(x), mx_of(w), Y, type == AAAC_F32, ldy, nullptr,
                                         false, (cudaStream_t)stream),
                    "aaac_mx_linear");
@@ -802,7 +799,6 @@ aaac_status aaac_mx_linear_ws(const aaac_mx_source* src, int64_t rows, const int
   x.K = w->K;
   x.offsets = offsets;
   if (own) {
-    aaac::count_launches(1);
     return from_cuda(aaac::launch_mx_gemm(x, mx_of(w), Y, type == AAAC_F32, ldy, &source, false,
                                           (cudaStream_t)stream),
                      "aaac_mx_linear_ws");
@@ -815,7 +811,6 @@ aaac_status aaac_mx_linear_ws(const aaac_mx_source* src, int64_t rows, const int
   if (e == cudaSuccess)
     e = aaac::launch_mx_gemm(x, mx_of(w), Y, type == AAAC_F32, ldy, nullptr, true,
                              (cudaStream_t)stream);
-  if (e == cudaSuccess) aaac::count_launches(2);
   return from_cuda(e, "aaac_mx_linear_ws");
 }
 

@@ -979,7 +979,9 @@ cudaError_t launch_t(const Maps& m, const MxGemmArgs& a, const MxPlan& p,
   n++;
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NT, MODE, SRC>, m.x, m.w, m.sx, m.sw, a, own);
+  e = cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NT, MODE, SRC>, m.x, m.w, m.sx, m.sw, a, own);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
 }
 
 template <int FMT, int MODE>

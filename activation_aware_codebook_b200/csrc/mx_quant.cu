@@ -198,7 +198,9 @@ cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, cudaSt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
 }
 
 // Runs a thread holds.  With many rows: enough that a block's loads cover the

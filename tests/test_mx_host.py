@@ -283,3 +283,20 @@ def test_workspace_of_fewer_bytes_than_elements_is_refused():
                torch.zeros(1 << 20, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError, match="contiguous"):
             bb.mx_linear(x, W, ws=ws)
+
+
+def test_launches_that_fail_are_not_counted(lib):
+    """kernel_launches counts kernels that were launched."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    x, w = tensor(), tensor()
+    few = source(rows=4)
+    before = bb.kernel_launches()
+    assert lib.aaac_mx_quantize(ref(source()), ref(x), None) == 5  # AAAC_ERR_CUDA
+    assert lib.aaac_mx_dequant(ref(x), FAKE, 1, 256, None) == 5
+    assert lib.aaac_mx_linear(ref(x), ref(w), FAKE, 1, 64, None) == 5
+    assert lib.aaac_mx_linear_ws(ref(source()), 64, None, ref(w), FAKE, 1, 64, FAKE, 1 << 40,
+                                 None) == 5
+    assert lib.aaac_mx_linear_ws(ref(few), 4, None, ref(w), FAKE, 1, 64, None, 0, None) == 5
+    assert bb.kernel_launches() == before
