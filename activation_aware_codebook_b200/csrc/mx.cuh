@@ -50,13 +50,6 @@ __device__ __forceinline__ uint32_t load_u8(const uint8_t* p) {
   asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint32_t load_u16(const uint16_t* p) {
-  uint32_t v;
-  asm volatile("{\n .reg .u16 h;\n ld.global.u16 h, [%1];\n cvt.u32.u16 %0, h;\n}\n"
-               : "=r"(v)
-               : "l"(p));
-  return v;
-}
 __device__ __forceinline__ float load_f32(const float* p) {
   float v;
   asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));

@@ -47,11 +47,6 @@ __device__ __forceinline__ Two mul2(Two a, Two b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.p), "l"(b.p));
   return Two(r);
 }
-__device__ __forceinline__ Two add2(Two a, Two b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.p), "l"(b.p));
-  return Two(r);
-}
 __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.p), "l"(b.p), "l"(c.p));
@@ -65,27 +60,22 @@ __device__ __forceinline__ Two neg_div_by(Two x, Two d, Two nr) {
   return fma2(nr, fma2(d, q, x), q);
 }
 
-// silu(a) b for two columns, each step in fp32; na = -a, at most kNear: up to
-// there 1 + exp(-a) is below 2^125, and its reciprocal a normal number.
-constexpr float kNear = 86.5f;
+// silu(a) b for two columns, each step in fp32; na = -a.  The quotient is taken
+// with (1 + exp(-a)) / 4, whose reciprocal is a normal number for every finite
+// exp(-a); the factor is exact.  An infinite exp(-a) (a < -88.72) has the
+// reciprocal 0 and the quotient -0; held finite in the residual it stays one,
+// and NaN comes of an infinite a alone.  Gates that far occur (an outlier
+// channel), and cost nothing here: a branch for them did, 39.5 us in place of
+// 36.8 for 4099 x 2 x 8192 to E4M3 (36.0 with no care for them).
 __device__ __forceinline__ void silu_mul(float na0, float na1, float b0, float b1, float& y0,
                                          float& y1) {
-  const Two d = add2(Two(1.0f), Two(expf(na0), expf(na1)));
+  const Two x(na0, na1);
+  const Two d = fma2(Two(0.25f), Two(expf(na0), expf(na1)), Two(0.25f));
   float d0, d1;
   d.get(d0, d1);
   const Two nr(-rcp_approx(d0), -rcp_approx(d1));
-  mul2(neg_div_by(Two(na0, na1), d, nr), Two(b0, b1)).get(y0, y1);
-}
-
-// The same for any a.  Where d = 1 + exp(-a) is large the quotient is taken
-// with the reciprocal of d / 16 and its power of two taken out, which is exact
-// (the quotient is above 86 / 2^128); 0 where d is infinite and a is not.
-__device__ __forceinline__ float silu_far(float a, float b) {
-  const float d = __fadd_rn(1.0f, expf(-a));
-  const float c = d > 0x1p124f ? 0x1p-4f : 1.0f;
-  const float t = __fmul_rn(d, c);
-  const float s = __fmul_rn(-div_by(-a, t, rcp_approx(t)), c);
-  return __fmul_rn(__float_as_uint(d) == 0x7f800000u && fabsf(a) < d ? -0.0f : s, b);
+  const Two s = neg_div_by(x, Two(fminf(d0, 0x1p126f), fminf(d1, 0x1p126f)), nr);
+  mul2(mul2(s, Two(0.25f)), Two(b0, b1)).get(y0, y1);
 }
 
 // 16 values of a row.  bf16 stays packed: half the registers.
@@ -124,34 +114,15 @@ struct Run {
       }
     }
   }
-  static __device__ __forceinline__ float load1(const void* X, int64_t at) {
-    if (F32) return load_f32(static_cast<const float*>(X) + at);
-    return __uint_as_float(load_u16(static_cast<const uint16_t*>(X) + at) << 16);
-  }
   // row_at: the source row's first element; col: this run's first column
   __device__ __forceinline__ void load(const void* X, int64_t row_at, int col, int K) {
     load16<SWIGLU>(X, row_at + col, v);
     if (SWIGLU) {
-      float u[16], most = 0.0f;
+      float u[16];
       load16<false>(X, row_at + K + col, u);
-      // A run with a gate below -kNear, which a trained network hardly has,
-      // takes its values from memory again, one at a time: a test a run in
-      // place of selects a value (SwiGLU of 4099 x 2 x 8192 to E4M3: bf16 36.2
-      // us with the test, 38.9 with selects; fp32 51.0 and 49.3).
 #pragma unroll
-      for (int i = 0; i < 16; i++) most = fmaxf(most, v[i]);
-      if (most > kNear) {
-        float t[16];
-#pragma unroll 1
-        for (int i = 0; i < 16; i++)
-          t[i] = silu_far(load1(X, row_at + col + i), load1(X, row_at + K + col + i));
-#pragma unroll
-        for (int i = 0; i < 16; i++) v[i] = t[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; i += 2)
-          silu_mul(v[i], v[i + 1], u[i], u[i + 1], v[i], v[i + 1]);
-      }
+      for (int i = 0; i < 16; i += 2)
+        silu_mul(v[i], v[i + 1], u[i], u[i + 1], v[i], v[i + 1]);
     }
   }
   // the largest magnitude's bits (a NaN or infinity is above every number)
