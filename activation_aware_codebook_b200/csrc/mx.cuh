@@ -5,8 +5,9 @@
 // byte along K, the low nibble the even column: the order in which tcgen05
 // reads packed 4-bit operands.  The block scales lie as the tensor core wants
 // them in tensor memory: tiles of 128 rows x 4 blocks, 512 bytes each, row
-// i's four bytes at (i % 32) * 16 + (i / 32) * 4, so that one 32x128b copy
-// brings a tile in without any thread touching it.  Tiles of a row band are
+// i's four bytes at (i % 32) * 16 + (i / 32) * 4.  Lane l's 16 bytes are then the
+// words of rows l, l + 32, l + 64 and l + 96, and a warp moves a tile there with
+// one load a lane and a store of four columns.  Tiles of a row band are
 // consecutive along K.
 #pragma once
 

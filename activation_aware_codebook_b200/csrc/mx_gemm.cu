@@ -187,7 +187,15 @@ __device__ __forceinline__ void commit_mx(uint64_t* bar) {
     mma_commit(bar);
 }
 
-// An arrival at the first CTA's barrier, from either CTA of a pair.
+// An arrival at the first CTA's barrier, from either CTA of a pair.  Its default
+// scope is the CTA, and it need not be more, for what it orders is no plain data:
+// tensor memory, by the tcgen05 fences before the arrival and after the wait, with
+// the stores and loads before it complete (tcgen05.wait); and code tiles in shared
+// memory, whose copies were complete (their barrier's wait) before the arrival and
+// which only the tensor core reads.  Nothing that threads write may be passed to
+// the other CTA under these barriers: that would take .release.cluster here and
+// .acquire.cluster at the wait, measured at twice the kernel's time (1800 against
+// 858 us at 2048 x 14336 x 65536).
 template <bool TWO>
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
   if (TWO) {
@@ -1024,10 +1032,14 @@ cudaError_t launch_f(const Maps& m, const MxGemmArgs& a, const MxPlan& p,
 
 }  // namespace
 
-// The plan with the least estimated time, in microseconds as measured at
-// N = 1024 to 14336, K = 4096 to 27648 and 128 to 2048 tokens (the estimate is
-// within a tenth there): a stage of a tile takes 0.20 + 0.0011 per token
-// column, of which the first part is the weight tile's way from L2 (narrow
+// The plan with the least estimated time, in microseconds, fitted at N = 1024 to
+// 14336, K = 4096 to 27648 and 128 to 2048 tokens.  A launch's start and end, 3 to 6
+// us that all plans share, are not in it (E4M3, in a graph, estimate and time: 2048
+// tokens by 14336 x 4096 53 and 56, by 4096 x 4096 15 and 21, by 1024 x 4096 6 and
+// 10; 333 by 5120 x 27648 35 and 41).  It does not know the format: E8M0, with half
+// the scales, takes up to a tenth less.  Where it is wrong: 300 tokens by 1024 x
+// 8192, 24 tiles split 6 ways, 6 and 23.  A stage of a tile takes 0.20 + 0.0011 per
+// token column, of which the first part is the weight tile's way from L2 (narrow
 // tiles pay it more often), and a tile's last stages and stores 0.5.  CTAs
 // that split a tile run one after the other where there are too many of them,
 // each with its start, and its joining of the parts, 4 for every 256 columns.

@@ -17,11 +17,14 @@
 // consecutive values (two 16-byte loads each) in registers between the row's
 // maximum and its codes, so a row is read once; a run is one E4M3 block, and
 // half an E8M0 one.  2 bytes in, 0.53 (E8M0) or 0.56 (E4M3) out per value.
-// Measured with a cold L2, of 6.55 TB/s: 8192 x 14336 bf16 to E8M0 53 us (5.6
-// TB/s), to E4M3 56 us (5.3 TB/s).  SwiGLU of 4099 x 2 x 8192 to E4M3 44 us (3.5
-// TB/s): 29 instructions a value, most of them expf, the divisions and unpacking;
-// they keep the issue slots 77% busy.
-// mx_dequant_kernel: 27648 x 5120 from E4M3 to bf16 59 us (6.1 TB/s).
+// Measured back to back in a graph, on inputs larger than L2, beside the time of
+// the bytes at 6.55 TB/s: 8192 x 14336 bf16 to E8M0 44 us (45), to E4M3 47 us (46);
+// from fp32 76 (81) and 89 (82).  SwiGLU of 4099 x 2 x 8192 bf16 to E8M0 31.5 us
+// (23), to E4M3 37 us (23): 28 instructions a value, most of them expf, the
+// divisions and unpacking, which keep the issue slots busy in 74% of the active
+// cycles; from fp32 45.5 and 50 (44).
+// mx_dequant_kernel: 27648 x 5120 from E4M3 to bf16 56 us (55), to fp32 98 us (99);
+// mx_dequant_ragged_kernel: 8192 x 14336 in 16 groups 50 us (46).
 #include "common.cuh"
 #include "internal.h"
 #include "mx.cuh"

@@ -29,8 +29,8 @@ __device__ __forceinline__ float div_by(float x, float d, float r) {
 }
 
 // Two values in a register pair: one instruction does for both what the scalar
-// one does for each, rounded alike (SwiGLU of 65536 x 2 x 2048 to E4M3: 148 us
-// in scalars, 134 in pairs).
+// one does for each, rounded alike (SwiGLU of 65536 x 2 x 2048 to E4M3, when this
+// was brought in: 148 us in scalars, 134 in pairs).
 struct Two {
   uint64_t p;
   __device__ __forceinline__ Two(float a, float b) {

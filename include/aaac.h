@@ -359,9 +359,9 @@ aaac_status aaac_linear_ws(const void* X, int64_t M, int64_t ldx, const uint8_t*
  * offsets is NULL, else rows offsets[e] .. offsets[e + 1] - 1 are group e's
  * (device int32 [groups + 1], ascending; groups may be empty; rows before
  * offsets[0] or from offsets[groups] on belong to none: no call writes
- * anything of theirs, and nothing depends on them).  Values of offsets outside [0, rows] are taken as the nearest
- * bound; descending ones give unspecified values, and every access stays in
- * bounds.
+ * anything of theirs, and nothing depends on them).  Values of offsets outside
+ * [0, rows] are taken as the nearest bound; descending ones give unspecified
+ * values and may leave rows unwritten, and every access stays in bounds.
  *   codes      [rows][K/2]: two per byte, low nibble = even k
  *   scales     aaac_mx_scale_bytes() bytes: tiles of 128 rows x 4 blocks, 512
  *              bytes each, row i's four bytes at (i % 32) * 16 + (i / 32) * 4;
@@ -391,7 +391,8 @@ size_t aaac_mx_scale_bytes(int32_t fmt, int64_t rows, int64_t K, int32_t groups)
  * when index is NULL).  An index outside [0, rows) gives a row of zeros, so
  * that -1 pads a batch.
  *   AAAC_MX_SWIGLU: X's rows hold two halves of K columns, a and b, and
- *     (a / (1 + exp(-a))) * b is quantised, computed in fp32. */
+ *     (a / (1 + exp(-a))) * b is quantised, computed in fp32: 0 times b where
+ *     exp(-a) is infinite (a < -88.72). */
 #define AAAC_MX_SWIGLU 1u
 typedef struct {
     const void* X;          /* device [rows][ldx], bf16 or fp32, 16-byte aligned rows */
@@ -406,7 +407,8 @@ typedef struct {
 aaac_status aaac_mx_quantize(const aaac_mx_source* src, const aaac_mx_tensor* q, void* stream);
 
 /* A tensor's values, E2M1 * scale * row_scale: exact in fp32 (6 significant
- * bits), and in bf16 inside its range.
+ * bits), and in bf16, inside their ranges; infinite beyond them (a block near
+ * the largest number whose scale was rounded up stands for more than that).
  *   out   device bf16 or fp32 [rows][ldo], rows 16-byte aligned */
 aaac_status aaac_mx_dequant(const aaac_mx_tensor* q, void* out, int32_t type, int64_t ldo,
                             void* stream);
