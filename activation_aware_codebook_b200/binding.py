@@ -505,7 +505,8 @@ def awq_fit(W: torch.Tensor, I: torch.Tensor, tokens: int, cfg: Config, alphas16
 
 
 # --------------------------------------------------------------------------
-# microscaled 4-bit tensors: quantisation, the way back, and the product
+# microscaled 4-bit tensors: quantisation, the way back, and the product (no
+# backward pass: outputs carry no gradient)
 # --------------------------------------------------------------------------
 MX_E8M0 = 0  # blocks of 32, power-of-two scales
 MX_E4M3 = 1  # blocks of 16, E4M3 scales, a power of two per row

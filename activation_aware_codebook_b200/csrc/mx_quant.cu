@@ -20,9 +20,9 @@
 // Measured back to back in a graph, on inputs larger than L2, beside the time of
 // the bytes at 6.55 TB/s: 8192 x 14336 bf16 to E8M0 44 us (45), to E4M3 47 us (46);
 // from fp32 76 (81) and 89 (82).  SwiGLU of 4099 x 2 x 8192 bf16 to E8M0 31.5 us
-// (23), to E4M3 37 us (23): 28 instructions a value, most of them expf, the
-// divisions and unpacking, which keep the issue slots busy in 74% of the active
-// cycles; from fp32 45.5 and 50 (44).
+// (23), to E4M3 37 us (23): 30 instructions a value, most of them expf, the
+// divisions and unpacking, which keep the issue slots busy in 75% of the active
+// cycles (67% of all); from fp32 45.5 and 50 (44).
 // mx_dequant_kernel: 27648 x 5120 from E4M3 to bf16 56 us (55), to fp32 98 us (99);
 // mx_dequant_ragged_kernel: 8192 x 14336 in 16 groups 50 us (46).
 #include "common.cuh"
