@@ -742,7 +742,8 @@ def _mx_quantize(X, fmt, rows, swiglu, groups, offsets, out, stream):
 
 def mx_dequant(q: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
-    """A microscaled tensor's values, bf16 or fp32 [rows, K]."""
+    """A microscaled tensor's values, bf16 or fp32 [rows, K] (rows of no group are
+    not written)."""
     if stream is not None:
         return _on_stream(_mx_dequant, stream, q, dtype, out, stream)
     return _mx_dequant(q, dtype, out, None)
@@ -765,7 +766,8 @@ def mx_linear(X: Union[torch.Tensor, MxTensor], W: MxTensor, out: Optional[torch
     group of X's rows (an expert's) meets its own N rows of W.  X is a
     microscaled tensor, or bf16 / fp32 activations that are quantised here as
     mx_quantize does (rows, swiglu and offsets as there; ws: a workspace of
-    mx_workspace_size bytes)."""
+    mx_workspace_size bytes).  Rows of no group are not written: without out
+    they hold anything."""
     if isinstance(X, MxTensor):
         if rows is not None or swiglu or offsets is not None or ws is not None:
             raise ValueError("rows, swiglu, offsets and ws go with activations that are not "
