@@ -32,12 +32,13 @@
 //     four times the measured bf16 rate.  MMAs alone take 145 us, copies alone
 //     158: together they share shared memory (38 KB written and 32 KB read a
 //     CTA and stage of 512 MMA cycles, of 128 bytes a cycle) and the power
-//     limit (sw_power_cap: 245 us with its quantisation in a long run).
-//   5120 x 27648 at 333 tokens: 40 us, 0.31 us a stage of 37 KB, the way from
+//     limit (up to 237 us in a long run, and 252 with its quantisation).
+//   5120 x 27648 at 333 tokens: 41 us, 0.31 us a stage of 37 KB, the way from
 //     L2 (copies alone 35).
-//   4096 x 4096 at one token: 7.1 us, of which 4.9 are a launch that loads and
-//     multiplies nothing.  64 experts of 2048 x 2048 at 128 rows: 22.6 us for
-//     133 MB, 0.9 of the measured HBM rate.
+//   4096 x 4096 at one token: 6.8 us, of which 4.9 are a launch that loads and
+//     multiplies nothing.  64 experts of 2048 x 2048, two rows each: 30 us for
+//     151 MB, 0.77 of the measured HBM rate; 128 rows over 45 of them 24.5 us for
+//     106 MB, 0.66: the start is the same.
 // What was measured on the way: scale tiles by tcgen05.cp cost 41 ns each, in
 // line with the MMAs (12 a stage: 0.49 us of 0.88); as bulk copies of 2 KB they
 // cost 90 ns each to fetch, as tensor copies 18; a lane on its own in place of
